@@ -233,8 +233,7 @@ def _calls(s):
         eps = _EPS[c["what"]]
         if c["what"] == "weights":
             return bl.fp8_quantize_weights(s["x"], eps, transposed=True)
-        rows = bl.fp8_quantize_act(s["x"], eps)
-        return rows if c["what"] == "act" else rows + bl.fp8_quantize_act_transposed(s["x"], eps)
+        return bl.fp8_quantize_act(s["x"], eps, transposed=c["what"] == "act_both")
     call = {"product": bl.fp8_forward, "grad_input": bl.fp8_backward_input, "grad_weight": bl.fp8_backward_weight}[op]
     return call(s["a"], s["sa"], s["b"], s["sb"], out_dtype=_T[c["y"]])
 
