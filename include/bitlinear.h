@@ -379,6 +379,128 @@ BL_API bl_status bitlinear_ste_backward_weight(const float *dY, const int8_t *xq
                                                const float *gamma, int64_t M, int64_t N, int64_t K, float *dW,
                                                void *stream);
 
+/* ----------------------------------------------------------------------------------
+ * The norm in front of a layer on its own, forward and backward.
+ * [BIN]: y = W~ . Quant(LN(x)).  bitlinear_norm_quantize_act fuses the norm with the int8
+ * quantiser; these give the normalised activations themselves (for layers that are left
+ * unternarised) and take a gradient at them -- what bitlinear_ste_backward_input or
+ * bitlinear_fp8_backward_input leaves -- on to x and to the norm's weight and bias.
+ *   mu = 0 (BL_NORM_RMS) or sum_k x_mk / K (BL_NORM_LAYER)
+ *   r = 1 / sqrt(sum_k (x_mk - mu)^2 / K + norm_eps);   n = (x_mk - mu) * r
+ *   forward:  y = n * w_k + b_k
+ *   backward: g = dy * w_k;  c1 = sum_k g n / K;  c2 = 0 (RMS) or sum_k g / K (LAYER)
+ *             dx = r * (g - c2 - n * c1);  dw_k = sum_m dy n;  db_k = sum_m dy
+ * All arithmetic and sums are fp32, rounded once to the output type; infinities and NaN
+ * spread to their row (and to the column sums) as the formulas say.  The sums run in an
+ * order fixed by the shape, so results repeat bit for bit.
+ * Types: x_dtype, y_dtype, dy_dtype, dx_dtype are each BL_OUT_F32 or BL_OUT_BF16.  Any
+ * K >= 1; M, K <= 2^30, M * K <= 2^40.  Rows are contiguous ([M, K] row-major); K % 8 == 0
+ * runs with 16-byte accesses.  Outputs must not overlap inputs or each other.
+ * ---------------------------------------------------------------------------------- */
+
+/*   X           in  : [M, K] of x_dtype, device.
+ *   norm_weight in  : fp32 [K], device, or NULL for 1.
+ *   norm_bias   in  : fp32 [K], device, or NULL for 0.
+ *   norm_eps    in  : >= 0, finite.
+ *   Y           out : [M, K] of y_dtype, device.
+ * Errors: BL_ERR_INVALID_ARG, BL_ERR_UNSUPPORTED_SHAPE, BL_ERR_MISALIGNED, BL_ERR_CUDA. */
+BL_API bl_status bitlinear_norm_forward(const void *X, bl_dtype x_dtype, const float *norm_weight,
+                                        const float *norm_bias, int64_t M, int64_t K, bl_norm_kind norm_kind,
+                                        float norm_eps, void *Y, bl_dtype y_dtype, void *stream);
+
+/* Bytes of device workspace bitlinear_norm_backward needs for an [M, K] matrix (partial
+ * column sums); 0 for shapes it refuses and for those that need none. */
+BL_API size_t bitlinear_norm_backward_workspace_size(int64_t M, int64_t K);
+
+/*   dY          in  : gradient at y, [M, K] of dy_dtype, device.
+ *   X, norm_weight, norm_kind, norm_eps: as in the forward (the statistics are taken from
+ *                     X again).  The bias does not enter.
+ *   dX          out : [M, K] of dx_dtype, device.
+ *   dweight     out : fp32 [K], device, or NULL; overwritten, not added to.
+ *   dbias       out : fp32 [K], device, or NULL.
+ *   ws, ws_bytes    : device workspace of at least bitlinear_norm_backward_workspace_size
+ *                     bytes, scratch for the duration of the enqueued work (calls that may
+ *                     run at the same time need one each).
+ * Errors: as the forward, and BL_ERR_WORKSPACE. */
+BL_API bl_status bitlinear_norm_backward(const void *dY, bl_dtype dy_dtype, const void *X, bl_dtype x_dtype,
+                                         const float *norm_weight, int64_t M, int64_t K, bl_norm_kind norm_kind,
+                                         float norm_eps, void *dX, bl_dtype dx_dtype, float *dweight, float *dbias,
+                                         void *ws, size_t ws_bytes, void *stream);
+
+/* ----------------------------------------------------------------------------------
+ * 8-bit floating-point product with a scale for each block of 128, for the layers of a
+ * b1.58 model that are left unternarised (an output head, or any matrix whose codes would
+ * not hold it), forward and backward.
+ * Codes are e4m3 bytes (sign, 4 exponent bits of bias 7, 3 fraction bits; largest 448; no
+ * infinity).  The quantisers take, for every block,
+ *   a = max |x| over the block,  m = max(a, eps),  d = m / 448,
+ *   code = e4m3(x * (448 / m))    (IEEE fp32 quotients and product, then one rounding to
+ *                                  nearest even; the largest element maps to +-448)
+ * and a code stands for code * d.  A block with an infinity or a NaN reads back as NaN.
+ *   activations  blocks of 128 elements along a row (the last one may be shorter):
+ *                codes [M, row_bytes(K)], scales fp32 [ceil(K / 128), M]
+ *   transposed   blocks of 128 tokens of a column, for the weight gradient's sum over the
+ *                tokens: codes [K, row_bytes(M)], scales fp32 [ceil(M / 128), K]
+ *   weights      blocks of 128 x 128: codes [N, row_bytes(K)], scales fp32
+ *                [ceil(N / 128), ceil(K / 128)]; transposed codes [K, row_bytes(N)] share
+ *                the scales (for the input gradient's sum over N)
+ * Rows of codes are padded to a multiple of 16 bytes; the quantisers write the padding as
+ * zeros and the products do not read it.  Any sizes from 1 up to 2^30 each (products of two up to 2^40).
+ * The products sum the exact products of codes in fp32 on the tensor cores, 128 at a time,
+ * scale every such sum by d_left * d_right in fp32 and add them in fp32, in an order fixed
+ * by the shape.
+ * ---------------------------------------------------------------------------------- */
+
+/* Bytes per row of K codes: K rounded up to a multiple of 16; 0 if K <= 0. */
+BL_API int64_t bitlinear_fp8_row_bytes(int64_t K);
+
+/* Quantise activations (or gradients) along their rows, their columns, or both in one pass.
+ *   X        in  : [M, K] of x_dtype (BL_OUT_F32 or BL_OUT_BF16), device.
+ *   eps      in  : >= 1e-30, finite.
+ *   xq_out, s_out   out : codes and scales along rows, or both NULL.
+ *   xqt_out, st_out out : transposed codes and scales along columns, or both NULL.
+ * Errors: BL_ERR_INVALID_ARG, BL_ERR_UNSUPPORTED_SHAPE, BL_ERR_MISALIGNED, BL_ERR_CUDA. */
+BL_API bl_status bitlinear_fp8_quantize_act(const void *X, bl_dtype x_dtype, int64_t M, int64_t K, float eps,
+                                            uint8_t *xq_out, float *s_out, uint8_t *xqt_out, float *st_out,
+                                            void *stream);
+
+/* Quantise a weight matrix in blocks of 128 x 128.
+ *   W        in  : [N, K] of w_dtype (BL_OUT_F32 or BL_OUT_BF16), device.
+ *   eps      in  : >= 1e-30, finite.
+ *   wq_out   out : codes [N, row_bytes(K)], or NULL.
+ *   s_out    out : fp32 [ceil(N / 128), ceil(K / 128)].
+ *   wqt_out  out : transposed codes [K, row_bytes(N)], or NULL (not both NULL).
+ * Errors: as bitlinear_fp8_quantize_act. */
+BL_API bl_status bitlinear_fp8_quantize_weights(const void *W, bl_dtype w_dtype, int64_t N, int64_t K, float eps,
+                                                uint8_t *wq_out, float *s_out, uint8_t *wqt_out, void *stream);
+
+/* y[m, n] = sum_k x[m, k] w[n, k] from codes.
+ *   xq, sx  in  : activations' codes [M, row_bytes(K)] and scales [ceil(K / 128), M].
+ *   wq, sw  in  : weights' codes [N, row_bytes(K)] and scales [ceil(N / 128), ceil(K / 128)].
+ *   out     out : [M, N] of out_dtype (BL_OUT_F32 or BL_OUT_BF16).
+ *   err_word out: optional; BL_ERRBIT_TIMEOUT if a bounded device wait gave up (the output
+ *                 is then incomplete).
+ * Errors: BL_ERR_INVALID_ARG, BL_ERR_UNSUPPORTED_SHAPE, BL_ERR_MISALIGNED, BL_ERR_CUDA. */
+BL_API bl_status bitlinear_fp8_forward(const uint8_t *xq, const float *sx, const uint8_t *wq, const float *sw,
+                                       int64_t M, int64_t N, int64_t K, void *out, bl_dtype out_dtype,
+                                       int32_t *err_word, void *stream);
+
+/* dX[m, k] = sum_n dY[m, n] w[n, k] from codes.
+ *   dyq, sdy in : the gradient's codes [M, row_bytes(N)] and scales [ceil(N / 128), M].
+ *   wqt, sw  in : transposed weight codes [K, row_bytes(N)] and the weights' scales.
+ *   dX      out : [M, K] of out_dtype.  The rest as for bitlinear_fp8_forward. */
+BL_API bl_status bitlinear_fp8_backward_input(const uint8_t *dyq, const float *sdy, const uint8_t *wqt,
+                                              const float *sw, int64_t M, int64_t N, int64_t K, void *dX,
+                                              bl_dtype out_dtype, int32_t *err_word, void *stream);
+
+/* dW[n, k] = sum_m dY[m, n] x[m, k] from transposed codes.
+ *   dyqt, sdyt in : codes [N, row_bytes(M)] and scales [ceil(M / 128), N].
+ *   xqt, sxt   in : codes [K, row_bytes(M)] and scales [ceil(M / 128), K].
+ *   dW        out : [N, K] of out_dtype.  The rest as for bitlinear_fp8_forward. */
+BL_API bl_status bitlinear_fp8_backward_weight(const uint8_t *dyqt, const float *sdyt, const uint8_t *xqt,
+                                               const float *sxt, int64_t M, int64_t N, int64_t K, void *dW,
+                                               bl_dtype out_dtype, int32_t *err_word, void *stream);
+
 /* CUDA error code (cudaError_t as int) of the last BL_ERR_CUDA on the calling thread. */
 BL_API int bitlinear_last_cuda_error(void);
 

@@ -12,6 +12,7 @@ allocate the output tensors with torch and call the entry points above.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -35,6 +36,9 @@ EXPORTED = [
     "bitlinear_forward_layout", "bitlinear_norm_quantize_act", "bitlinear_forward_rowscale",
     "bitlinear_tl5_row_bytes", "bitlinear_pack_tl5", "bitlinear_repack_tl5", "bitlinear_forward_tl5",
     "bitlinear_ste_backward_input", "bitlinear_ste_backward_weight", "bitlinear_forward_stall_test",
+    "bitlinear_norm_forward", "bitlinear_norm_backward_workspace_size", "bitlinear_norm_backward",
+    "bitlinear_fp8_row_bytes", "bitlinear_fp8_quantize_act", "bitlinear_fp8_quantize_weights",
+    "bitlinear_fp8_forward", "bitlinear_fp8_backward_input", "bitlinear_fp8_backward_weight",
     "bitlinear_last_cuda_error",
     "bitlinear_status_string",
 ]
@@ -100,6 +104,24 @@ def lib() -> ctypes.CDLL:
         L.bitlinear_forward_stall_test.argtypes = [P, P, P, P, I64, I64, I64, P, S, P, S, S, ctypes.c_uint64,
                                                    ctypes.c_int32, P]
         L.bitlinear_forward_stall_test.restype = S
+        L.bitlinear_norm_forward.argtypes = [P, S, P, P, I64, I64, S, F, P, S, P]
+        L.bitlinear_norm_forward.restype = S
+        L.bitlinear_norm_backward_workspace_size.argtypes = [I64, I64]
+        L.bitlinear_norm_backward_workspace_size.restype = ctypes.c_size_t
+        L.bitlinear_norm_backward.argtypes = [P, S, P, S, P, I64, I64, S, F, P, S, P, P, P, ctypes.c_size_t, P]
+        L.bitlinear_norm_backward.restype = S
+        L.bitlinear_fp8_row_bytes.argtypes = [I64]
+        L.bitlinear_fp8_row_bytes.restype = I64
+        L.bitlinear_fp8_quantize_act.argtypes = [P, S, I64, I64, F, P, P, P, P, P]
+        L.bitlinear_fp8_quantize_act.restype = S
+        L.bitlinear_fp8_quantize_weights.argtypes = [P, S, I64, I64, F, P, P, P, P]
+        L.bitlinear_fp8_quantize_weights.restype = S
+        L.bitlinear_fp8_forward.argtypes = [P, P, P, P, I64, I64, I64, P, S, P, P]
+        L.bitlinear_fp8_forward.restype = S
+        L.bitlinear_fp8_backward_input.argtypes = [P, P, P, P, I64, I64, I64, P, S, P, P]
+        L.bitlinear_fp8_backward_input.restype = S
+        L.bitlinear_fp8_backward_weight.argtypes = [P, P, P, P, I64, I64, I64, P, S, P, P]
+        L.bitlinear_fp8_backward_weight.restype = S
         L.bitlinear_last_cuda_error.argtypes = []
         L.bitlinear_last_cuda_error.restype = ctypes.c_int
         L.bitlinear_status_string.argtypes = [ctypes.c_int]
@@ -285,6 +307,144 @@ def bitlinear_ste_backward_weight(dY, xq, s, gamma, dW, stream=None):
         "bitlinear_ste_backward_weight")
 
 
+# The norm and e4m3 calls run on the device of their tensors (all on one), whichever is
+# current, and on its current stream or the one given.
+
+_FLOATS = {torch.float32: BL_OUT_F32, torch.bfloat16: BL_OUT_BF16}
+_E4M3 = torch.float8_e4m3fn
+_HERE_ALREADY = contextlib.nullcontext()
+
+
+def _scope(stream, *tensors):
+    """A context in which the tensors' device, and `stream` if given, are current."""
+    device = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError("every tensor must be a CUDA tensor")
+        if device is None:
+            device = t.device
+        elif t.device != device:
+            raise ValueError("tensors must be on one device, got %s and %s" % (device, t.device))
+    if stream is None:
+        return _HERE_ALREADY if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    if stream.device != device:
+        raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, device))
+    return torch.cuda.stream(stream)
+
+
+def _float(t: torch.Tensor, name: str, shape=None):
+    """(pointer, bl_dtype) of an fp32 or bf16 tensor."""
+    kind = _FLOATS.get(t.dtype) if isinstance(t, torch.Tensor) else None
+    if kind is None:
+        raise TypeError("%s must be float32 or bfloat16" % name)
+    return _dev(t, t.dtype, name, shape), kind
+
+
+def _vec(t, name, K):
+    return None if t is None else _dev(t, torch.float32, name, (K,))
+
+
+def _matrix(t, name):
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError("%s must be a matrix" % name)
+    return t.shape
+
+
+def _blocks(n: int) -> int:
+    return -(-n // 128)
+
+
+def bitlinear_norm_forward(X, norm_weight, norm_bias, kind, norm_eps, out, stream=None):
+    M, K = _matrix(X, "X")
+    with _scope(stream, X, norm_weight, norm_bias, out):
+        _check(lib().bitlinear_norm_forward(
+            *_float(X, "X"), _vec(norm_weight, "norm_weight", K), _vec(norm_bias, "norm_bias", K), M, K, int(kind),
+            float(norm_eps), *_float(out, "out", (M, K)), _stream(None)), "bitlinear_norm_forward")
+
+
+def bitlinear_norm_backward_workspace_size(M: int, K: int) -> int:
+    return int(lib().bitlinear_norm_backward_workspace_size(int(M), int(K)))
+
+
+def bitlinear_norm_backward(dY, X, norm_weight, kind, norm_eps, dX, dweight, dbias, ws, stream=None):
+    M, K = _matrix(X, "X")
+    with _scope(stream, X, dY, norm_weight, dX, dweight, dbias, ws):
+        _check(lib().bitlinear_norm_backward(
+            *_float(dY, "dY", (M, K)), *_float(X, "X"), _vec(norm_weight, "norm_weight", K), M, K, int(kind),
+            float(norm_eps), *_float(dX, "dX", (M, K)), _vec(dweight, "dweight", K), _vec(dbias, "dbias", K),
+            None if ws is None else _dev(ws, torch.uint8, "ws"), 0 if ws is None else ws.numel(), _stream(None)),
+            "bitlinear_norm_backward")
+
+
+def bitlinear_fp8_row_bytes(K: int) -> int:
+    return int(lib().bitlinear_fp8_row_bytes(int(K)))
+
+
+def bitlinear_fp8_quantize_act(X, eps, xq_out, s_out, xqt_out=None, st_out=None, stream=None):
+    M, K = _matrix(X, "X")
+    with _scope(stream, X, xq_out, s_out, xqt_out, st_out):
+        _check(lib().bitlinear_fp8_quantize_act(
+            *_float(X, "X"), M, K, float(eps),
+            None if xq_out is None else _dev(xq_out, _E4M3, "xq_out", (M, bitlinear_fp8_row_bytes(K))),
+            None if s_out is None else _dev(s_out, torch.float32, "s_out", (_blocks(K), M)),
+            None if xqt_out is None else _dev(xqt_out, _E4M3, "xqt_out", (K, bitlinear_fp8_row_bytes(M))),
+            None if st_out is None else _dev(st_out, torch.float32, "st_out", (_blocks(M), K)), _stream(None)),
+            "bitlinear_fp8_quantize_act")
+
+
+def bitlinear_fp8_quantize_weights(W, eps, wq_out, s_out, wqt_out=None, stream=None):
+    N, K = _matrix(W, "W")
+    with _scope(stream, W, wq_out, s_out, wqt_out):
+        _check(lib().bitlinear_fp8_quantize_weights(
+            *_float(W, "W"), N, K, float(eps),
+            None if wq_out is None else _dev(wq_out, _E4M3, "wq_out", (N, bitlinear_fp8_row_bytes(K))),
+            _dev(s_out, torch.float32, "s_out", (_blocks(N), _blocks(K))),
+            None if wqt_out is None else _dev(wqt_out, _E4M3, "wqt_out", (K, bitlinear_fp8_row_bytes(N))),
+            _stream(None)), "bitlinear_fp8_quantize_weights")
+
+
+def _codes_of(left, right, names):
+    """Rows of two code matrices and the bytes of their rows.  The padding behind a row is
+    zero, so the padded length serves as the contraction's."""
+    rows_l, n = _matrix(left, names[0])
+    rows_r, n_r = _matrix(right, names[1])
+    if n != n_r or n % 16 != 0:
+        raise ValueError("%s and %s must have rows of the same multiple of 16 codes, got %d and %d"
+                         % (*names, n, n_r))
+    return rows_l, rows_r, n
+
+
+def bitlinear_fp8_forward(xq, sx, wq, sw, out, err_word=None, stream=None):
+    M, N, K = _codes_of(xq, wq, ("xq", "wq"))
+    with _scope(stream, xq, sx, wq, sw, out, err_word):
+        _check(lib().bitlinear_fp8_forward(
+            _dev(xq, _E4M3, "xq"), _dev(sx, torch.float32, "sx", (_blocks(K), M)), _dev(wq, _E4M3, "wq"),
+            _dev(sw, torch.float32, "sw", (_blocks(N), _blocks(K))), M, N, K, *_float(out, "out", (M, N)),
+            _opt(err_word, "err_word"), _stream(None)), "bitlinear_fp8_forward")
+
+
+def bitlinear_fp8_backward_input(dyq, sdy, wqt, sw, dX, err_word=None, stream=None):
+    M, K, N = _codes_of(dyq, wqt, ("dyq", "wqt"))
+    with _scope(stream, dyq, sdy, wqt, sw, dX, err_word):
+        _check(lib().bitlinear_fp8_backward_input(
+            _dev(dyq, _E4M3, "dyq"), _dev(sdy, torch.float32, "sdy", (_blocks(N), M)), _dev(wqt, _E4M3, "wqt"),
+            _dev(sw, torch.float32, "sw", (_blocks(N), _blocks(K))), M, N, K, *_float(dX, "dX", (M, K)),
+            _opt(err_word, "err_word"), _stream(None)), "bitlinear_fp8_backward_input")
+
+
+def bitlinear_fp8_backward_weight(dyqt, sdyt, xqt, sxt, dW, err_word=None, stream=None):
+    N, K, M = _codes_of(dyqt, xqt, ("dyqt", "xqt"))
+    with _scope(stream, dyqt, sdyt, xqt, sxt, dW, err_word):
+        _check(lib().bitlinear_fp8_backward_weight(
+            _dev(dyqt, _E4M3, "dyqt"), _dev(sdyt, torch.float32, "sdyt", (_blocks(M), N)), _dev(xqt, _E4M3, "xqt"),
+            _dev(sxt, torch.float32, "sxt", (_blocks(M), K)), M, N, K, *_float(dW, "dW", (N, K)),
+            _opt(err_word, "err_word"), _stream(None)), "bitlinear_fp8_backward_weight")
+
+
 # ----------------------------------------------------------- allocating helpers --
 
 def quantize_weights(W: torch.Tensor, eps: float = 1e-5, stream=None):
@@ -356,3 +516,80 @@ def ste_backward(dY, packed, xq, s, gamma, stream=None):
     bitlinear_ste_backward_input(dY, packed, gamma, dX, stream)
     bitlinear_ste_backward_weight(dY, xq, s, gamma, dW, stream)
     return dX, dW
+
+
+def norm_forward(X: torch.Tensor, norm_weight=None, norm_bias=None, kind=BL_NORM_RMS, norm_eps: float = 1e-5,
+                 out_dtype=None, stream=None):
+    """RMSNorm / LayerNorm(X) [M, K] of an fp32 or bf16 CUDA matrix, as out_dtype (X's by default)."""
+    with _scope(stream, X):
+        out = torch.empty(X.shape, dtype=out_dtype or X.dtype, device=X.device)
+        bitlinear_norm_forward(X, norm_weight, norm_bias, kind, norm_eps, out)
+    return out
+
+
+def norm_backward(dY: torch.Tensor, X: torch.Tensor, norm_weight=None, kind=BL_NORM_RMS, norm_eps: float = 1e-5,
+                  bias: bool = False, dx_dtype=None, stream=None):
+    """(dX [M, K], dweight [K] fp32, dbias [K] fp32) of norm_forward for the gradient dY at its
+    result.  dX is dx_dtype (dY's type by default); dweight is None without a norm_weight,
+    dbias unless `bias`."""
+    M, K = _matrix(X, "X")
+    with _scope(stream, X, dY):
+        dX = torch.empty(M, K, dtype=dx_dtype or dY.dtype, device=X.device)
+        dw = torch.empty(K, dtype=torch.float32, device=X.device) if norm_weight is not None else None
+        db = torch.empty(K, dtype=torch.float32, device=X.device) if bias else None
+        n = bitlinear_norm_backward_workspace_size(M, K)
+        ws = torch.empty(n, dtype=torch.uint8, device=X.device) if n else None
+        bitlinear_norm_backward(dY, X, norm_weight, kind, norm_eps, dX, dw, db, ws)
+    return dX, dw, db
+
+
+def fp8_quantize_act(X: torch.Tensor, eps: float = 1e-5, transposed: bool = False, stream=None):
+    """(xq, sx) of an fp32 or bf16 CUDA matrix: e4m3 codes [M, K rounded up to 16] and one fp32
+    scale per 128 elements of a row [ceil(K/128), M].  With `transposed` also (xqt, sxt), the
+    codes [K, M rounded up to 16] with one scale per 128 elements of a column."""
+    M, K = _matrix(X, "X")
+    with _scope(stream, X):
+        out = [torch.empty(M, bitlinear_fp8_row_bytes(K), dtype=_E4M3, device=X.device),
+               torch.empty(_blocks(K), M, dtype=torch.float32, device=X.device)]
+        if transposed:
+            out += [torch.empty(K, bitlinear_fp8_row_bytes(M), dtype=_E4M3, device=X.device),
+                    torch.empty(_blocks(M), K, dtype=torch.float32, device=X.device)]
+        bitlinear_fp8_quantize_act(X, eps, *out)
+    return tuple(out)
+
+
+def fp8_quantize_weights(W: torch.Tensor, eps: float = 1e-5, transposed: bool = False, stream=None):
+    """(wq, sw) of an fp32 or bf16 CUDA weight matrix: e4m3 codes [N, K rounded up to 16] and one
+    fp32 scale per 128 x 128 block.  With `transposed` also wqt, the codes [K, N rounded up to 16]."""
+    N, K = _matrix(W, "W")
+    with _scope(stream, W):
+        out = [torch.empty(N, bitlinear_fp8_row_bytes(K), dtype=_E4M3, device=W.device),
+               torch.empty(_blocks(N), _blocks(K), dtype=torch.float32, device=W.device)]
+        if transposed:
+            out.append(torch.empty(K, bitlinear_fp8_row_bytes(N), dtype=_E4M3, device=W.device))
+        bitlinear_fp8_quantize_weights(W, eps, *out)
+    return tuple(out)
+
+
+def fp8_forward(xq, sx, wq, sw, out_dtype=torch.float32, stream=None, err_word=None):
+    """y [M, N] = x w^T from the codes and scales of fp8_quantize_act and fp8_quantize_weights."""
+    with _scope(stream, xq):
+        out = torch.empty(xq.shape[0], wq.shape[0], dtype=out_dtype, device=xq.device)
+        bitlinear_fp8_forward(xq, sx, wq, sw, out, err_word)
+    return out
+
+
+def fp8_backward_input(dyq, sdy, wqt, sw, out_dtype=torch.float32, stream=None, err_word=None):
+    """dX [M, K] = dY w from the gradient's codes and the transposed weight codes."""
+    with _scope(stream, dyq):
+        dX = torch.empty(dyq.shape[0], wqt.shape[0], dtype=out_dtype, device=dyq.device)
+        bitlinear_fp8_backward_input(dyq, sdy, wqt, sw, dX, err_word)
+    return dX
+
+
+def fp8_backward_weight(dyqt, sdyt, xqt, sxt, out_dtype=torch.float32, stream=None, err_word=None):
+    """dW [N, K] = dY^T x from the transposed codes of the gradient and the activations."""
+    with _scope(stream, dyqt):
+        dW = torch.empty(dyqt.shape[0], xqt.shape[0], dtype=out_dtype, device=dyqt.device)
+        bitlinear_fp8_backward_weight(dyqt, sdyt, xqt, sxt, dW, err_word)
+    return dW

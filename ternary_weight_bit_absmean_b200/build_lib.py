@@ -21,8 +21,9 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libbitlinear.so")
 DEBUG_LIB = os.path.join(PKG, "libbitlinear_debug.so")
-SOURCES = ["bl_api.cu", "k_quant.cu", "k_gemv.cu", "k_gemv_tma.cu", "k_gemv_tc.cu", "k_gemv_stream.cu", "k_gemm_tc.cu", "k_gemm_tc2.cu", "bl_noalloc.cu", "k_tl5.cu", "k_ste.cu"]
-HEADERS = ["bl_device.cuh", "bl_internal.h"]
+SOURCES = ["bl_api.cu", "k_quant.cu", "k_gemv.cu", "k_gemv_tma.cu", "k_gemv_tc.cu", "k_gemv_stream.cu", "k_gemm_tc.cu", "k_gemm_tc2.cu", "bl_noalloc.cu", "k_tl5.cu", "k_ste.cu",
+           "k_norm.cu", "k_fp8_quant.cu", "k_fp8_gemm.cu"]
+HEADERS = ["bl_device.cuh", "bl_fp8.cuh", "bl_internal.h"]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
@@ -65,15 +66,19 @@ def build(force: bool = False, verbose: bool = False, debug: bool = False) -> st
         return lib
     objdir = os.path.join(PKG, "_build_debug" if debug else "_build")
     os.makedirs(objdir, exist_ok=True)
-    objs = []
-    for src in SOURCES:
+    objs, running = [], []
+    for src in SOURCES:  # one compiler per file, side by side
         obj = os.path.join(objdir, src.replace(".cu", ".o"))
         cmd = [NVCC, *FLAGS, *(["-DBL_DEBUG_CHECKS=1"] if debug else []), "-I", INCLUDE, "-I", CSRC, "-c",
                os.path.join(CSRC, src), "-o", obj]
         if verbose:
             cmd.insert(1, "-Xptxas=-v")
-        subprocess.run(cmd, check=True)
+        running.append((cmd, subprocess.Popen(cmd)))
         objs.append(obj)
+    # wait for all of them before complaining about one
+    for cmd, code in [(cmd, proc.wait()) for cmd, proc in running]:
+        if code != 0:
+            raise subprocess.CalledProcessError(code, cmd)
     tmp = lib + ".tmp.%d" % os.getpid()
     subprocess.run([NVCC, "-shared", "-gencode", "arch=compute_100a,code=sm_100a", "-cudart", "static",
                     *objs, "-o", tmp], check=True)

@@ -8,6 +8,7 @@
 #include <cuda_runtime.h>
 
 #include "bitlinear.h"
+#include "bl_fp8.cuh"
 #include "bl_internal.h"
 
 namespace {
@@ -344,6 +345,133 @@ bl_status bitlinear_forward(const int8_t* xq, const float* s, const uint8_t* pac
                             int32_t* err_word, void* stream) {
     return bitlinear_forward_path(xq, s, packed, gamma, M, N, K, out, out_dtype, err_word, BL_PATH_AUTO,
                                   stream);
+}
+
+// Floating-point types of the norm and e4m3 entry points.
+static bool float_dtype(bl_dtype t) { return t == BL_OUT_F32 || t == BL_OUT_BF16; }
+
+// Row and column counts shared by those entry points.
+static bl_status check_float_shape(int64_t rows, int64_t cols) {
+    if (rows <= 0 || cols <= 0) return BL_ERR_INVALID_ARG;
+    const int64_t lim = int64_t(1) << 30;
+    if (rows > lim || cols > lim || rows > (int64_t(1) << 40) / cols) return BL_ERR_UNSUPPORTED_SHAPE;
+    return BL_OK;
+}
+
+static bl_status check_norm(bl_norm_kind kind, float norm_eps) {
+    if (kind != BL_NORM_RMS && kind != BL_NORM_LAYER) return BL_ERR_INVALID_ARG;
+    if (!std::isfinite(norm_eps) || norm_eps < 0.0f) return BL_ERR_INVALID_ARG;
+    return BL_OK;
+}
+
+bl_status bitlinear_norm_forward(const void* X, bl_dtype x_dtype, const float* norm_weight, const float* norm_bias,
+                                 int64_t M, int64_t K, bl_norm_kind norm_kind, float norm_eps, void* Y,
+                                 bl_dtype y_dtype, void* stream) {
+    BL_RANGE("bitlinear_norm_forward");
+    if (X == nullptr || Y == nullptr || !float_dtype(x_dtype) || !float_dtype(y_dtype)) return BL_ERR_INVALID_ARG;
+    bl_status st = check_norm(norm_kind, norm_eps);
+    if (st != BL_OK) return st;
+    st = check_float_shape(M, K);
+    if (st != BL_OK) return st;
+    if (!aligned16(X) || !aligned16(Y) || !aligned16(norm_weight) || !aligned16(norm_bias)) return BL_ERR_MISALIGNED;
+    return cuda_status(bl::launch_norm_forward(X, x_dtype == BL_OUT_BF16, norm_weight, norm_bias, M, K,
+                                               static_cast<int>(norm_kind), norm_eps, Y, y_dtype == BL_OUT_BF16,
+                                               as_stream(stream)));
+}
+
+size_t bitlinear_norm_backward_workspace_size(int64_t M, int64_t K) {
+    return check_float_shape(M, K) == BL_OK ? bl::norm_backward_workspace(M, K) : 0;
+}
+
+bl_status bitlinear_norm_backward(const void* dY, bl_dtype dy_dtype, const void* X, bl_dtype x_dtype,
+                                  const float* norm_weight, int64_t M, int64_t K, bl_norm_kind norm_kind,
+                                  float norm_eps, void* dX, bl_dtype dx_dtype, float* dweight, float* dbias, void* ws,
+                                  size_t ws_bytes, void* stream) {
+    BL_RANGE("bitlinear_norm_backward");
+    if (dY == nullptr || X == nullptr || dX == nullptr) return BL_ERR_INVALID_ARG;
+    if (!float_dtype(dy_dtype) || !float_dtype(x_dtype) || !float_dtype(dx_dtype)) return BL_ERR_INVALID_ARG;
+    bl_status st = check_norm(norm_kind, norm_eps);
+    if (st != BL_OK) return st;
+    st = check_float_shape(M, K);
+    if (st != BL_OK) return st;
+    if (!aligned16(dY) || !aligned16(X) || !aligned16(norm_weight) || !aligned16(dX) || !aligned16(dweight) ||
+        !aligned16(dbias))
+        return BL_ERR_MISALIGNED;
+    const size_t need = bl::norm_backward_workspace(M, K);
+    if (need > 0 && (ws == nullptr || ws_bytes < need)) return BL_ERR_WORKSPACE;
+    if (!aligned16(ws)) return BL_ERR_MISALIGNED;
+    return cuda_status(bl::launch_norm_backward(dY, dy_dtype == BL_OUT_BF16, X, x_dtype == BL_OUT_BF16, norm_weight, M,
+                                                K, static_cast<int>(norm_kind), norm_eps, dX, dx_dtype == BL_OUT_BF16,
+                                                dweight, dbias, ws, as_stream(stream)));
+}
+
+int64_t bitlinear_fp8_row_bytes(int64_t K) { return K <= 0 ? 0 : bl::fp8_row_bytes(K); }
+
+// 448 / eps and eps / 448 have to stay ordinary fp32 numbers.
+static bool fp8_eps_ok(float eps) { return std::isfinite(eps) && eps >= 1e-30f; }
+
+bl_status bitlinear_fp8_quantize_act(const void* X, bl_dtype x_dtype, int64_t M, int64_t K, float eps, uint8_t* xq_out,
+                                     float* s_out, uint8_t* xqt_out, float* st_out, void* stream) {
+    BL_RANGE("bitlinear_fp8_quantize_act");
+    if (X == nullptr || !float_dtype(x_dtype) || !fp8_eps_ok(eps)) return BL_ERR_INVALID_ARG;
+    if ((xq_out == nullptr) != (s_out == nullptr) || (xqt_out == nullptr) != (st_out == nullptr))
+        return BL_ERR_INVALID_ARG;
+    if (xq_out == nullptr && xqt_out == nullptr) return BL_ERR_INVALID_ARG;
+    const bl_status st = check_float_shape(M, K);
+    if (st != BL_OK) return st;
+    if (!aligned16(X) || !aligned16(xq_out) || !aligned16(s_out) || !aligned16(xqt_out) || !aligned16(st_out))
+        return BL_ERR_MISALIGNED;
+    return cuda_status(bl::launch_fp8_quantize_act(X, x_dtype == BL_OUT_BF16, M, K, eps, xq_out, s_out, xqt_out,
+                                                   st_out, as_stream(stream)));
+}
+
+bl_status bitlinear_fp8_quantize_weights(const void* W, bl_dtype w_dtype, int64_t N, int64_t K, float eps,
+                                         uint8_t* wq_out, float* s_out, uint8_t* wqt_out, void* stream) {
+    BL_RANGE("bitlinear_fp8_quantize_weights");
+    if (W == nullptr || !float_dtype(w_dtype) || !fp8_eps_ok(eps)) return BL_ERR_INVALID_ARG;
+    if (s_out == nullptr || (wq_out == nullptr && wqt_out == nullptr)) return BL_ERR_INVALID_ARG;
+    const bl_status st = check_float_shape(N, K);
+    if (st != BL_OK) return st;
+    if (!aligned16(W) || !aligned16(wq_out) || !aligned16(s_out) || !aligned16(wqt_out)) return BL_ERR_MISALIGNED;
+    return cuda_status(bl::launch_fp8_quantize_weights(W, w_dtype == BL_OUT_BF16, N, K, eps, wq_out, s_out, wqt_out,
+                                                       as_stream(stream)));
+}
+
+// The three products differ in what is contracted and in how the right operand is scaled.
+static bl_status fp8_product(const uint8_t* q, const float* sq, const uint8_t* p, const float* sp, int64_t Q,
+                             int64_t P, int64_t C, int64_t sp_p, int64_t sp_g, int p_shift, void* out,
+                             bl_dtype out_dtype, int32_t* err_word, void* stream) {
+    if (q == nullptr || sq == nullptr || p == nullptr || sp == nullptr || out == nullptr || !float_dtype(out_dtype))
+        return BL_ERR_INVALID_ARG;
+    bl_status st = check_float_shape(Q, C);
+    if (st == BL_OK) st = check_float_shape(P, C);
+    if (st == BL_OK) st = check_float_shape(Q, P);
+    if (st != BL_OK) return st;
+    if (!aligned16(q) || !aligned16(sq) || !aligned16(p) || !aligned16(sp) || !aligned16(out))
+        return BL_ERR_MISALIGNED;
+    const bl::Fp8Product d{q, p, Q, P, C, sq, sp, sp_p, sp_g, p_shift, out, out_dtype == BL_OUT_BF16 ? 1 : 0, err_word};
+    return cuda_status(bl::launch_fp8_product(d, as_stream(stream)));
+}
+
+bl_status bitlinear_fp8_forward(const uint8_t* xq, const float* sx, const uint8_t* wq, const float* sw, int64_t M,
+                                int64_t N, int64_t K, void* out, bl_dtype out_dtype, int32_t* err_word, void* stream) {
+    BL_RANGE("bitlinear_fp8_forward");
+    // sw [N blocks, K blocks]: rows of w are the output columns, K is contracted
+    return fp8_product(xq, sx, wq, sw, M, N, K, (K + 127) / 128, 1, 7, out, out_dtype, err_word, stream);
+}
+
+bl_status bitlinear_fp8_backward_input(const uint8_t* dyq, const float* sdy, const uint8_t* wqt, const float* sw,
+                                       int64_t M, int64_t N, int64_t K, void* dX, bl_dtype out_dtype,
+                                       int32_t* err_word, void* stream) {
+    BL_RANGE("bitlinear_fp8_backward_input");
+    return fp8_product(dyq, sdy, wqt, sw, M, K, N, 1, (K + 127) / 128, 7, dX, out_dtype, err_word, stream);
+}
+
+bl_status bitlinear_fp8_backward_weight(const uint8_t* dyqt, const float* sdyt, const uint8_t* xqt, const float* sxt,
+                                        int64_t M, int64_t N, int64_t K, void* dW, bl_dtype out_dtype,
+                                        int32_t* err_word, void* stream) {
+    BL_RANGE("bitlinear_fp8_backward_weight");
+    return fp8_product(dyqt, sdyt, xqt, sxt, N, K, M, 1, K, 0, dW, out_dtype, err_word, stream);
 }
 
 int bitlinear_last_cuda_error(void) { return g_last_cuda_error; }

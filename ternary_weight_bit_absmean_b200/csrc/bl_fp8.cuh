@@ -1,0 +1,83 @@
+// bl_fp8.cuh -- building blocks of the 8-bit floating-point product kernels: the
+// tcgen05 kind::f8f6f4 MMA, packed fp32 arithmetic, small asynchronous copies, and the
+// description of one block-scaled product shared by the kernels.
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "bl_device.cuh"
+
+namespace bl {
+
+// D[tmem] (+)= A[smem] * B[smem]^T on 8-bit floats, fp32 accumulation, issued by one thread.
+__device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Instruction descriptor: kind::f8f6f4, A and B e4m3, K-major, D fp32, shape M x N.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
+    return (1u << 4)                                 // D format: F32 (A and B formats 0: e4m3)
+           | (static_cast<uint32_t>(N >> 3) << 17)   // N / 8
+           | (static_cast<uint32_t>(M >> 4) << 24);  // M / 16
+}
+
+// Two fp32 values in one 64-bit register pair, for the packed multiply and fma.
+__device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 unpack_f32x2(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// Copy 4 bytes global -> shared without a register; and have this thread arrive on `bar`
+// when all of its copies so far have landed (one of the barrier's expected arrivals).
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// One product of the library in the kernels' terms:
+//   out[q, p] = sum_g sq[g, q] sp(g, p) sum_{c in group g} Qm[q, c] Pm[p, c]
+// Qm is the left operand of the public entry points (tokens, or rows of W for the weight
+// gradient), Pm the right one; both hold e4m3 codes with the contraction index c
+// innermost and groups of 128 of it.  sq has one scale per row of Qm; sp one per row
+// (p_shift 0) or one per 128 rows (p_shift 7): sp[(p >> p_shift) * sp_p + g * sp_g].
+struct Fp8Product {
+    const uint8_t* q;
+    const uint8_t* p;
+    int64_t Q, P, C;
+    const float* sq;
+    const float* sp;
+    int64_t sp_p, sp_g;
+    int p_shift;
+    void* out;      // [Q, P]
+    int out_bf16;
+    int32_t* err;
+};
+
+}  // namespace bl

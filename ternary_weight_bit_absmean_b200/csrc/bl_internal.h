@@ -133,6 +133,28 @@ cudaError_t launch_ste_grad_input(const float* dY, const uint8_t* packed, const 
 cudaError_t launch_ste_grad_weight(const float* dY, const int8_t* xq, const float* s, const float* gamma, int64_t M,
                                    int64_t N, int64_t K, float* dW, cudaStream_t stream);
 
+// RMSNorm (kind 0) / LayerNorm (kind 1) alone, forward and backward (k_norm.cu).  The
+// backward's partial column sums live in `ws` (norm_backward_workspace bytes).
+cudaError_t launch_norm_forward(const void* X, bool x_bf16, const float* w, const float* b, int64_t M, int64_t K,
+                                int kind, float eps, void* Y, bool y_bf16, cudaStream_t stream);
+size_t norm_backward_workspace(int64_t M, int64_t K);
+cudaError_t launch_norm_backward(const void* dY, bool dy_bf16, const void* X, bool x_bf16, const float* w, int64_t M,
+                                 int64_t K, int kind, float eps, void* dX, bool dx_bf16, float* dw, float* db,
+                                 void* ws, cudaStream_t stream);
+
+// e4m3 codes with one scale per block of 128 (k_fp8_quant.cu): rows of codes are
+// fp8_row_bytes(K) apart.  Activations: codes and scales along rows (q, s) and / or along
+// columns, transposed (qt, st); weights: 128 x 128 blocks, codes in either orientation.
+int64_t fp8_row_bytes(int64_t K);
+cudaError_t launch_fp8_quantize_act(const void* X, bool x_bf16, int64_t M, int64_t K, float eps, uint8_t* q, float* s,
+                                    uint8_t* qt, float* st, cudaStream_t stream);
+cudaError_t launch_fp8_quantize_weights(const void* W, bool w_bf16, int64_t N, int64_t K, float eps, uint8_t* q,
+                                        float* s, uint8_t* qt, cudaStream_t stream);
+
+// The product of such matrices (Fp8Product in bl_fp8.cuh; k_fp8_gemm.cu).
+struct Fp8Product;
+cudaError_t launch_fp8_product(const Fp8Product& d, cudaStream_t stream);
+
 // Keep a CUDA error code for bitlinear_last_cuda_error() on the calling thread.
 void record_cuda_error(int code);
 

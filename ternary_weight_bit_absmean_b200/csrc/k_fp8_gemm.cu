@@ -1,0 +1,398 @@
+// k_fp8_gemm.cu -- the product of e4m3 matrices with one scale for each block of 128
+// (tcgen05.mma kind::f8f6f4, fp32 accumulators in tensor memory), for single tokens up to
+// middling batches.  It serves layers left unternarised next to the BitLinear ones, and
+// both gradients of such a layer.
+//
+//   out[q, p] = sum_g sq[g, q] sp(g, p) S_g[q, p],   S_g[q, p] = sum_{c in group g} Qm[q, c] Pm[p, c]
+//
+// The scales change every 128 elements of the contraction, so the tensor cores sum one
+// group (four MMAs of K = 32) into a fresh accumulator, and the epilogue warps read it
+// back, multiply by the two scales and add it to fp32 sums in registers, while the tensor
+// cores work on the next group in another accumulator.  Products of e4m3 values are exact
+// in fp32.
+//
+// Tile: 128 rows of Pm (MMA M, TMEM lanes) x BQ rows of Qm (MMA N): with one token the
+// 128-row weight tiles are what is streamed, and the outputs of a warp are 32 neighbours
+// of an output row.  Per group of 128:
+//   warp 0 (one lane)  TMA: 128 x 128 bytes of Pm, BQ x 128 bytes of Qm (128-byte swizzle);
+//   warp 1 (one lane)  MMA issuer;
+//   warp 2             scales: 4-byte asynchronous copies into a ring of eight groups;
+//   warps 4 ..         epilogue: a thread owns one row of Pm (its TMEM lane) and a range of
+//                      the BQ columns.
+// With few tiles the groups are split over the blocks of a cluster, which add their
+// partial sums through distributed shared memory in a fixed order.  All waits are bounded
+// as in the ternary kernels; a block that gives up drains its copies and MMAs, sets
+// BL_ERRBIT_TIMEOUT and still takes part in the cluster barriers.
+#include <cuda_bf16.h>
+#include <cstdint>
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_runtime.h>
+
+#include "bl_device.cuh"
+#include "bl_fp8.cuh"
+#include "bl_internal.h"
+
+namespace bl {
+
+// 2-D tensor map over rows of `inner` bytes that start every `pitch` bytes, 128-byte
+// swizzle, zero fill outside; encoded anew by every call.
+bool encode_tmap_u8_pitch(CUtensorMap* map, const void* ptr, uint64_t inner, uint64_t outer, uint64_t pitch,
+                          uint32_t box_inner, uint32_t box_outer) {
+    struct Encode {
+        PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+        Encode() {
+            void* p = nullptr;
+            cudaDriverEntryPointQueryResult q;
+            if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+                    cudaSuccess &&
+                q == cudaDriverEntryPointSuccess)
+                fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+        }
+    };
+    static const Encode encode;  // looked up once (thread-safe static initialisation)
+    if (encode.fn == nullptr) return false;
+    const cuuint64_t dims[2] = {inner, outer};
+    const cuuint64_t strides[1] = {pitch};
+    const cuuint32_t box[2] = {box_inner, box_outer};
+    const cuuint32_t estr[2] = {1, 1};
+    return encode.fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+namespace {
+
+constexpr int kRows = 128;  // rows of Pm per tile
+constexpr int kG = 128;     // contraction elements (bytes) per group and stage
+constexpr int kWarpTma = 0, kWarpMma = 1, kWarpScale = 2, kWarpEpi = 4;
+constexpr int kScaleSlots = 8;
+constexpr int kMaxCluster = 8;
+constexpr unsigned long long kDrainNs = 200000000ull;  // 0.2 s
+
+template <int BQ>
+struct Cfg {
+    static constexpr int kEpiWarps = BQ >= 128 ? 8 : 4;
+    static constexpr int kThreads = 32 * (kWarpEpi + kEpiWarps);
+    static constexpr int kCols = BQ / (kEpiWarps / 4);  // columns of an epilogue thread
+    static constexpr int kQBytes = BQ * kG;
+    static constexpr int kPBytes = kRows * kG;
+    static constexpr int kStageBytes = kQBytes + kPBytes;
+    // tiles of up to 64 rows of Qm leave room for a second block on the SM, whose loads run
+    // on while this one starts, reduces and stores
+    static constexpr int kStages = BQ >= 128 ? 6 : BQ == 64 ? 4 : 5;
+    static constexpr int kBufs = BQ >= 128 ? 2 : 4;  // TMEM accumulators
+    static constexpr int kTmemCols = BQ * kBufs;
+    static constexpr int kSlotFloats = BQ + kRows;
+    static constexpr int kScaleBytes = kScaleSlots * kSlotFloats * 4;
+    static constexpr int kBars = 2 * kStages + 2 * kBufs + 2 * kScaleSlots + 1;
+    static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kScaleBytes + 8 * kBars + 16;
+    static_assert(BQ * kRows * 4 <= kStages * kStageBytes, "partial sums alias the stages");
+    static_assert(kTmemCols >= 32 && kTmemCols <= (BQ >= 128 ? 512 : 256), "tensor memory of the resident blocks");
+    static_assert(kSmemBytes <= (BQ >= 128 ? 227 : 113) * 1024, "shared memory of the resident blocks");
+};
+
+struct Args {
+    Fp8Product d;
+    int groups;            // of the contraction
+    int groups_per_split;  // of a block of the cluster (the last takes the rest)
+    int tiles_q;
+};
+
+__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
+    const unsigned long long t0 = globaltimer_ns();
+    while (!mbar_try_wait(bar, parity)) {
+        if (globaltimer_ns() - t0 > kDrainNs) return;
+    }
+}
+
+__device__ __forceinline__ float ld_shared_cluster_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void store_one(const Fp8Product& d, int64_t q, int64_t p, float v) {
+    if (d.out_bf16)
+        static_cast<__nv_bfloat16*>(d.out)[q * d.P + p] = __float2bfloat16_rn(v);
+    else
+        static_cast<float*>(d.out)[q * d.P + p] = v;
+}
+
+// grid: x = (tile, block of the cluster), tiles ordered with the Qm tiles of one Pm tile
+// next to each other (they read the same Pm rows, from L2 after the first).
+template <int BQ>
+__global__ void __launch_bounds__(Cfg<BQ>::kThreads)
+    fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_p,
+                    const Args a, const int nsplit) {
+    using C = Cfg<BQ>;
+    constexpr int ST = C::kStages, NB = C::kBufs;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t* gbase = smem_raw + (base - raw);
+    const uint32_t sP = base;
+    const uint32_t sQ = sP + ST * C::kPBytes;
+    const uint32_t sScale = sQ + ST * C::kQBytes;
+    const uint32_t sBar = sScale + C::kScaleBytes;
+    auto full = [&](int s) { return sBar + 8u * s; };                 // stage landed
+    auto empty = [&](int s) { return sBar + 8u * (ST + s); };         // stage read by the MMAs
+    auto tfull = [&](int b) { return sBar + 8u * (2 * ST + b); };     // accumulator holds a group
+    auto tempty = [&](int b) { return sBar + 8u * (2 * ST + NB + b); };  // accumulator read
+    auto sfull = [&](int s) { return sBar + 8u * (2 * ST + 2 * NB + s); };
+    auto sempty = [&](int s) { return sBar + 8u * (2 * ST + 2 * NB + kScaleSlots + s); };
+    const uint32_t drain_bar = sBar + 8u * (C::kBars - 1);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + (sBar - base) + 8 * C::kBars);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    float* scales = reinterpret_cast<float*>(gbase + (sScale - base));
+    float* red = reinterpret_cast<float*>(gbase);  // [BQ][128] partial sums, after the main loop
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int split = blockIdx.x % nsplit;
+    const int tile = blockIdx.x / nsplit;
+    const int64_t p0 = static_cast<int64_t>(tile / a.tiles_q) * kRows;
+    const int64_t q0 = static_cast<int64_t>(tile % a.tiles_q) * BQ;
+    const int g0 = split * a.groups_per_split;
+    const int ng = (split + 1 == nsplit ? a.groups : g0 + a.groups_per_split) - g0;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < ST; ++s) {
+            mbar_init(full(s), 1);
+            mbar_init(empty(s), 1);
+        }
+        for (int b = 0; b < NB; ++b) {
+            mbar_init(tfull(b), 1);
+            mbar_init(tempty(b), C::kEpiWarps);
+        }
+        for (int s = 0; s < kScaleSlots; ++s) {
+            mbar_init(sfull(s), 32);
+            mbar_init(sempty(s), C::kEpiWarps);
+        }
+        mbar_init(drain_bar, 1);
+        *abort_flag = 0;
+        mbar_fence_init();
+        tma_prefetch_desc(&tmap_q);
+        tma_prefetch_desc(&tmap_p);
+    }
+    pdl_wait_then_release();
+    if (warp == kWarpMma) {
+        tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+
+    if (warp == kWarpTma) {
+        if (lane == 0) {
+            // ------------------------------------------------------------ producer --
+            long long issued = 0;
+            bool ok = true;
+            for (int i = 0; i < ng; ++i) {
+                const int stage = i % ST;
+                if (!mbar_wait_bounded(empty(stage), static_cast<uint32_t>(((i / ST) & 1) ^ 1), abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                mbar_arrive_expect_tx(full(stage), C::kStageBytes);
+                tma_load_2d(sP + stage * C::kPBytes, &tmap_p, full(stage), (g0 + i) * kG, static_cast<int>(p0));
+                tma_load_2d(sQ + stage * C::kQBytes, &tmap_q, full(stage), (g0 + i) * kG, static_cast<int>(q0));
+                ++issued;
+            }
+            if (!ok) {
+                // wait for every load still in flight before the block may go on
+                for (int s = 0; s < ST; ++s) {
+                    const long long fills = (issued - s + ST - 1) / ST;
+                    if (fills > 0) drain_wait(full(s), static_cast<uint32_t>((fills - 1) & 1));
+                }
+            }
+        }
+    } else if (warp == kWarpMma) {
+        if (lane == 0) {
+            // ---------------------------------------------------------- MMA issuer --
+            constexpr uint32_t idesc = idesc_e4m3(kRows, BQ);
+            bool ok = true;
+            for (int i = 0; i < ng; ++i) {
+                const int stage = i % ST, buf = i % NB;
+                if (!mbar_wait_bounded(tempty(buf), static_cast<uint32_t>(((i / NB) & 1) ^ 1), abort_flag) ||
+                    !mbar_wait_bounded(full(stage), static_cast<uint32_t>((i / ST) & 1), abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t pa = sP + stage * C::kPBytes, qa = sQ + stage * C::kQBytes;
+#pragma unroll
+                for (int kk = 0; kk < kG / 32; ++kk)
+                    tc_mma_f8(tmem_base + static_cast<uint32_t>(buf * BQ), smem_desc_sw128(pa + 32 * kk),
+                              smem_desc_sw128(qa + 32 * kk), idesc, kk != 0 ? 1u : 0u);
+                tc_commit(empty(stage));
+                tc_commit(tfull(buf));
+            }
+            if (!ok) {
+                tc_commit(drain_bar);
+                drain_wait(drain_bar, 0);
+            }
+        }
+    } else if (warp == kWarpScale) {
+        // -------------------------------------------------------------- scales --
+        // rows past an edge take the last row's scale; they are not stored
+        for (int i = 0; i < ng; ++i) {
+            const int slot = i % kScaleSlots;
+            if (!mbar_wait_bounded(sempty(slot), static_cast<uint32_t>(((i / kScaleSlots) & 1) ^ 1), abort_flag))
+                break;
+            const uint32_t dst = sScale + static_cast<uint32_t>(slot * C::kSlotFloats * 4);
+            const int64_t g = g0 + i;
+#pragma unroll
+            for (int c = 0; c < BQ; c += 32) {
+                const int j = c + lane;
+                const int64_t q = q0 + j < a.d.Q ? q0 + j : a.d.Q - 1;
+                if (BQ >= 32 || j < BQ) cp_async4(dst + 4u * j, a.d.sq + g * a.d.Q + q);
+            }
+#pragma unroll
+            for (int c = 0; c < kRows; c += 32) {
+                const int j = c + lane;
+                const int64_t p = p0 + j < a.d.P ? p0 + j : a.d.P - 1;
+                cp_async4(dst + 4u * (BQ + j), a.d.sp + (p >> a.d.p_shift) * a.d.sp_p + g * a.d.sp_g);
+            }
+            cp_async_arrive(sfull(slot));
+        }
+        cp_async_wait_all();
+    } else if (warp >= kWarpEpi) {
+        // ------------------------------------------------------------ epilogue --
+        const int quarter = warp & 3, c_begin = ((warp - kWarpEpi) >> 2) * C::kCols;
+        const int r = 32 * quarter + lane;
+        const uint32_t lane_addr = static_cast<uint32_t>(32 * quarter) << 16;
+        uint64_t acc[C::kCols / 2];
+#pragma unroll
+        for (int j = 0; j < C::kCols / 2; ++j) acc[j] = 0;
+        bool ok = true;
+        for (int i = 0; i < ng; ++i) {
+            const int slot = i % kScaleSlots, buf = i % NB;
+            if (!mbar_wait_bounded(sfull(slot), static_cast<uint32_t>((i / kScaleSlots) & 1), abort_flag) ||
+                !mbar_wait_bounded(tfull(buf), static_cast<uint32_t>((i / NB) & 1), abort_flag)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const float* sc = scales + slot * C::kSlotFloats;
+            const uint64_t sp2 = pack_f32x2(sc[BQ + r], sc[BQ + r]);
+            uint32_t v[C::kCols / 16][16];
+#pragma unroll
+            for (int c = 0; c < C::kCols / 16; ++c)
+                tmem_ld_32x32b_x16(tmem_base + lane_addr + static_cast<uint32_t>(buf * BQ + c_begin + 16 * c), v[c]);
+            tmem_ld_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(tempty(buf));
+#pragma unroll
+            for (int j = 0; j < C::kCols / 4; ++j) {
+                const float4 s4 = *reinterpret_cast<const float4*>(sc + c_begin + 4 * j);
+                const uint32_t* w = &v[j / 4][4 * (j % 4)];
+                acc[2 * j] = fma_f32x2(pack_f32x2(__uint_as_float(w[0]), __uint_as_float(w[1])),
+                                       mul_f32x2(sp2, pack_f32x2(s4.x, s4.y)), acc[2 * j]);
+                acc[2 * j + 1] = fma_f32x2(pack_f32x2(__uint_as_float(w[2]), __uint_as_float(w[3])),
+                                           mul_f32x2(sp2, pack_f32x2(s4.z, s4.w)), acc[2 * j + 1]);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(sempty(slot));
+        }
+        if (ok) {
+            // with a split, every stage of this block has been read (its last group is in
+            // the sums), so the partial sums may take the stages' place
+#pragma unroll
+            for (int j = 0; j < C::kCols; ++j) {
+                const float2 two = unpack_f32x2(acc[j / 2]);
+                const float y = j % 2 == 0 ? two.x : two.y;
+                if (nsplit > 1) {
+                    red[(c_begin + j) * kRows + r] = y;
+                } else {
+                    const int64_t q = q0 + c_begin + j, p = p0 + r;
+                    if (q < a.d.Q && p < a.d.P) store_one(a.d, q, p, y);
+                }
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (nsplit > 1) {
+        // every block's partial sums are in its shared memory: block b adds, for the rows
+        // q with q % nsplit == b, the sums of all blocks in their order
+        cluster_sync_all();
+        const int rr = threadIdx.x & (kRows - 1);
+        const int64_t p = p0 + rr;
+        const uint32_t red_addr = smem_u32(red);
+        for (int j = split + nsplit * (threadIdx.x / kRows); j < BQ; j += nsplit * (C::kThreads / kRows)) {
+            const int64_t q = q0 + j;
+            if (q >= a.d.Q || p >= a.d.P) continue;
+            float sum = 0.0f;
+            for (int b = 0; b < nsplit; ++b)
+                sum += ld_shared_cluster_f32(mapa_shared(red_addr + 4u * (j * kRows + rr), b));
+            store_one(a.d, q, p, sum);
+        }
+        // no block leaves while another may still read its shared memory
+        cluster_sync_all();
+    }
+    if (warp == kWarpMma) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, C::kTmemCols);
+    }
+    if (threadIdx.x == 0 && *abort_flag && a.d.err != nullptr) atomicOr(a.d.err, kErrBitTimeout);
+}
+
+int sm_count() {
+    int dev = 0, sms = 148;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    return sms;
+}
+
+template <int BQ>
+cudaError_t launch_bq(const Fp8Product& d, cudaStream_t stream) {
+    using C = Cfg<BQ>;
+    const int64_t tiles_p = (d.P + kRows - 1) / kRows, tiles_q = (d.Q + BQ - 1) / BQ;
+    const int groups = static_cast<int>((d.C + kG - 1) / kG);
+    // the split with the fewest waves x (groups of a block + its start, reduction and
+    // stores, about eight groups' time)
+    const int64_t slots = static_cast<int64_t>(sm_count()) * (BQ >= 128 ? 1 : 2);
+    const int64_t tiles = tiles_p * tiles_q;
+    int64_t split = 1, best = -1;
+    for (int64_t sp = 1; sp <= kMaxCluster && sp <= groups; ++sp) {
+        const int64_t waves = (tiles * sp + slots - 1) / slots;
+        const int64_t cost = waves * ((groups + sp - 1) / sp + 8);
+        if (best < 0 || cost < best) {
+            best = cost;
+            split = sp;
+        }
+    }
+    const int64_t per = (groups + split - 1) / split;
+    split = (groups + per - 1) / per;  // every block has at least one group
+    if (tiles * split >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
+    CUtensorMap tq, tp;
+    if (!encode_tmap_u8_pitch(&tq, d.q, static_cast<uint64_t>(d.C), static_cast<uint64_t>(d.Q),
+                              static_cast<uint64_t>(fp8_row_bytes(d.C)), kG, BQ) ||
+        !encode_tmap_u8_pitch(&tp, d.p, static_cast<uint64_t>(d.C), static_cast<uint64_t>(d.P),
+                              static_cast<uint64_t>(fp8_row_bytes(d.C)), kG, kRows))
+        return cudaErrorInvalidValue;
+    static PerContextOnce attr;
+    cudaError_t e = attr.run([] {
+        return cudaFuncSetAttribute(fp8_gemm_kernel<BQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+    });
+    if (e != cudaSuccess) return e;
+    const Args a{d, groups, static_cast<int>(per), static_cast<int>(tiles_q)};
+    return launch_pdl(fp8_gemm_kernel<BQ>, dim3(static_cast<unsigned>(tiles * split)), dim3(C::kThreads),
+                      C::kSmemBytes, stream, split > 1 ? dim3(static_cast<unsigned>(split), 1, 1) : dim3(kNoCluster),
+                      tq, tp, a, static_cast<int>(split));
+}
+
+}  // namespace
+
+cudaError_t launch_fp8_product(const Fp8Product& d, cudaStream_t stream) {
+    if (d.Q <= 16) return launch_bq<16>(d, stream);
+    if (d.Q <= 32) return launch_bq<32>(d, stream);
+    if (d.Q <= 64) return launch_bq<64>(d, stream);
+    return launch_bq<128>(d, stream);
+}
+
+}  // namespace bl
