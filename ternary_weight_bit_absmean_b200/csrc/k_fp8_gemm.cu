@@ -281,7 +281,8 @@ __global__ void __launch_bounds__(Cfg<BQ>::kThreads)
 #pragma unroll
             for (int c = 0; c < C::kCols / 16; ++c)
                 tmem_ld_32x32b_x16(tmem_base + lane_addr + static_cast<uint32_t>(buf * BQ + c_begin + 16 * c), v[c]);
-            tmem_ld_wait();
+#pragma unroll
+            for (int c = 0; c < C::kCols / 16; ++c) tmem_ld_wait_for(v[c]);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(tempty(buf));
@@ -388,7 +389,10 @@ cudaError_t launch_bq(const Fp8Product& d, cudaStream_t stream) {
 
 }  // namespace
 
+cudaError_t launch_fp8_product_pair(const Fp8Product& d, cudaStream_t stream);
+
 cudaError_t launch_fp8_product(const Fp8Product& d, cudaStream_t stream) {
+    if (d.Q > 128) return launch_fp8_product_pair(d, stream);
     if (d.Q <= 16) return launch_bq<16>(d, stream);
     if (d.Q <= 32) return launch_bq<32>(d, stream);
     if (d.Q <= 64) return launch_bq<64>(d, stream);

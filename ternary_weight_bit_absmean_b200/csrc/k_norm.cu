@@ -454,13 +454,6 @@ __global__ void __launch_bounds__(1024)
     if (threadIdx.x == 0 && ko < K) out[ko] = v;
 }
 
-int sm_count() {
-    int dev = 0, sms = 148;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    return sms;
-}
-
 // Threads of a row and row groups of a block for rows of K elements in CH chunks a thread.
 struct Shape {
     int tpr, groups;
