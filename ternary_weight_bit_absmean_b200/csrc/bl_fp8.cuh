@@ -94,6 +94,18 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
 }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
+// True in one lane of a converged warp.  Instructions with warp-uniform operands (MMAs, commits,
+// TMA loads) are cheap to issue under it; under a test of the lane number they are not.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
 // One product of the library in the kernels' terms:
 //   out[q, p] = sum_g sq[g, q] sp(g, p) sum_{c in group g} Qm[q, c] Pm[p, c]
 // Qm is the left operand of the public entry points (tokens, or rows of W for the weight

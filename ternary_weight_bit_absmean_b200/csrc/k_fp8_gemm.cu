@@ -14,8 +14,8 @@
 // Tile: 128 rows of Pm (MMA M, TMEM lanes) x BQ rows of Qm (MMA N): with one token the
 // 128-row weight tiles are what is streamed, and the outputs of a warp are 32 neighbours
 // of an output row.  Per group of 128:
-//   warp 0 (one lane)  TMA: 128 x 128 bytes of Pm, BQ x 128 bytes of Qm (128-byte swizzle);
-//   warp 1 (one lane)  MMA issuer;
+//   warp 0             TMA: 128 x 128 bytes of Pm, BQ x 128 bytes of Qm (128-byte swizzle);
+//   warp 1             MMA issuer;
 //   warp 2             scales: 4-byte asynchronous copies into a ring of eight groups;
 //   warps 4 ..         epilogue: a thread owns one row of Pm (its TMEM lane) and a range of
 //                      the BQ columns.
@@ -185,54 +185,57 @@ __global__ void __launch_bounds__(Cfg<BQ>::kThreads)
     const uint32_t tmem_base = *tmem_slot;
 
     if (warp == kWarpTma) {
-        if (lane == 0) {
-            // ------------------------------------------------------------ producer --
-            long long issued = 0;
-            bool ok = true;
-            for (int i = 0; i < ng; ++i) {
-                const int stage = i % ST;
-                if (!mbar_wait_bounded(empty(stage), static_cast<uint32_t>(((i / ST) & 1) ^ 1), abort_flag)) {
-                    ok = false;
-                    break;
-                }
+        // ---------------------------------------------------------------- producer --
+        long long issued = 0;
+        bool ok = true;
+        for (int i = 0; i < ng; ++i) {
+            const int stage = i % ST;
+            if (!mbar_wait_bounded(empty(stage), static_cast<uint32_t>(((i / ST) & 1) ^ 1), abort_flag)) {
+                ok = false;
+                break;
+            }
+            if (elect_one()) {
                 mbar_arrive_expect_tx(full(stage), C::kStageBytes);
                 tma_load_2d(sP + stage * C::kPBytes, &tmap_p, full(stage), (g0 + i) * kG, static_cast<int>(p0));
                 tma_load_2d(sQ + stage * C::kQBytes, &tmap_q, full(stage), (g0 + i) * kG, static_cast<int>(q0));
-                ++issued;
             }
-            if (!ok) {
-                // wait for every load still in flight before the block may go on
-                for (int s = 0; s < ST; ++s) {
-                    const long long fills = (issued - s + ST - 1) / ST;
-                    if (fills > 0) drain_wait(full(s), static_cast<uint32_t>((fills - 1) & 1));
-                }
+            __syncwarp();
+            ++issued;
+        }
+        if (!ok) {
+            // wait for every load still in flight before the block may go on
+            for (int s = 0; s < ST; ++s) {
+                const long long fills = (issued - s + ST - 1) / ST;
+                if (fills > 0) drain_wait(full(s), static_cast<uint32_t>((fills - 1) & 1));
             }
         }
     } else if (warp == kWarpMma) {
-        if (lane == 0) {
-            // ---------------------------------------------------------- MMA issuer --
-            constexpr uint32_t idesc = idesc_e4m3(kRows, BQ);
-            bool ok = true;
-            for (int i = 0; i < ng; ++i) {
-                const int stage = i % ST, buf = i % NB;
-                if (!mbar_wait_bounded(tempty(buf), static_cast<uint32_t>(((i / NB) & 1) ^ 1), abort_flag) ||
-                    !mbar_wait_bounded(full(stage), static_cast<uint32_t>((i / ST) & 1), abort_flag)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
+        // -------------------------------------------------------------- MMA issuer --
+        constexpr uint32_t idesc = idesc_e4m3(kRows, BQ);
+        bool ok = true;
+        for (int i = 0; i < ng; ++i) {
+            const int stage = i % ST, buf = i % NB;
+            if (!mbar_wait_bounded(full(stage), static_cast<uint32_t>((i / ST) & 1), abort_flag) ||
+                !mbar_wait_bounded(tempty(buf), static_cast<uint32_t>(((i / NB) & 1) ^ 1), abort_flag)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            if (elect_one()) {
                 const uint32_t pa = sP + stage * C::kPBytes, qa = sQ + stage * C::kQBytes;
 #pragma unroll
                 for (int kk = 0; kk < kG / 32; ++kk)
                     tc_mma_f8(tmem_base + static_cast<uint32_t>(buf * BQ), smem_desc_sw128(pa + 32 * kk),
                               smem_desc_sw128(qa + 32 * kk), idesc, kk != 0 ? 1u : 0u);
-                tc_commit(empty(stage));
                 tc_commit(tfull(buf));
+                tc_commit(empty(stage));
             }
-            if (!ok) {
-                tc_commit(drain_bar);
-                drain_wait(drain_bar, 0);
-            }
+            __syncwarp();
+        }
+        if (!ok) {
+            if (elect_one()) tc_commit(drain_bar);
+            __syncwarp();
+            drain_wait(drain_bar, 0);
         }
     } else if (warp == kWarpScale) {
         // -------------------------------------------------------------- scales --

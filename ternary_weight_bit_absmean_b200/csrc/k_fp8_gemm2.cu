@@ -10,13 +10,20 @@
 // scale it and add it to fp32 sums in registers (a thread owns one row and 128 columns).
 // What a tile needs per group and SM: 512 cycles of the tensor pipe, 128 KB read from tensor
 // memory, 32768 fp32 multiply-adds (256 cycles of the fp32 pipe; twice that when both sides
-// are scaled by row), 64 KB through shared memory.  The tensor pipe is meant to be the bound.
+// are scaled by row), 64 KB through shared memory.
 //
-// Roles per CTA (12 warps): warp 0 lane 0 issues the TMA loads (signalled on the even CTA's
-// barrier), warp 1 lane 0 of the even CTA the MMAs, warp 2 copies scales into a ring of eight
-// groups, warps 4-11 run the epilogue.  The register file is split by setmaxnreg: the first
-// four warps give up what the epilogue's sums need.  All waits are bounded as in the
-// ternary kernels; no load uses multicast.
+// Roles per CTA (12 warps): warp 0 issues the TMA loads (signalled on the even CTA's barrier),
+// warp 1 of the even CTA the MMAs, warp 2 copies scales into a ring of eight groups, warps
+// 4-11 run the epilogue.  Loads and MMAs are issued by an elected lane of a warp whose lanes
+// all run the loop: issued from a branch of one lane, four MMAs and two commits took 590
+// cycles against 230, more than the tensor pipe needs for them.  The register file is split
+// by setmaxnreg.  All waits are bounded as in the ternary kernels; no load uses multicast.
+//
+// Measured (bf16 output): 8192 x 8640 x 3200 in 217 us, 2.08 PFLOP/s; with the epilogue taken
+// out, loads and MMAs alone run at 3.05.  What is left is the hand-over of the two
+// accumulators (an accumulator is busy for its MMAs, the commit, the readers' 430 cycles and
+// their signal back: about 1660 cycles for two groups on an idle GPU) and the clock, which
+// the power limit lowers.
 #include <cuda_bf16.h>
 #include <cstdint>
 #include <cuda.h>
@@ -38,15 +45,18 @@ constexpr int kTile = 2 * kHalf;
 constexpr int kG = 128;
 constexpr int kThreads = 384;
 constexpr int kWarpTma = 0, kWarpMma = 1, kWarpScale = 2, kWarpEpi = 4, kEpiWarps = 8;
+constexpr int kCols = kTile / (kEpiWarps / 4);  // columns of an epilogue thread
 constexpr int kOpBytes = kHalf * kG;  // one operand's half per stage: 16 KB
 constexpr int kStages = 6;
 constexpr int kSlots = 8;             // scale ring
 constexpr int kSlotFloats = kHalf + kTile;
+constexpr int kTurnBytes = 2048;      // of an epilogue warp: 32 rows x 64 bytes of output
 constexpr int kBars = 2 * kStages + 4 + 2 * kSlots + 1;
-constexpr int kSmemBytes = 1024 + kStages * 2 * kOpBytes + kSlots * kSlotFloats * 4 + 8 * kBars + 16;
+constexpr int kSmemBytes =
+    1024 + kStages * 2 * kOpBytes + kEpiWarps * kTurnBytes + kSlots * kSlotFloats * 4 + 8 * kBars + 16;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
-// 128 threads give up registers for the 256 of the epilogue: 128 * 56 + 256 * 224 is
-// the 384 * 168 that the block is launched with
+// the first four warps give up registers for the epilogue's sums: 128 * 56 + 256 * 224 is the
+// 384 * 168 that the block is launched with
 constexpr int kRegsLaunch = 168, kRegsSmall = 56, kRegsEpi = 224;
 static_assert(128 * kRegsSmall + 256 * kRegsEpi <= kThreads * kRegsLaunch, "register split");
 constexpr unsigned long long kDrainNs = 200000000ull;
@@ -76,41 +86,63 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
     }
 }
 
-__device__ __forceinline__ uint32_t pack_bf16(float2 v) {
-    const __nv_bfloat162 p = __floats2bfloat162_rn(v.x, v.y);
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&p);
 }
 
-// 128 sums of one row -> out[q, p .. p + 127], 16-byte stores when the row allows them.
-__device__ __forceinline__ void store_row(const Fp8Product& d, int64_t q, int64_t p, const uint64_t (&acc)[64]) {
-    if (q >= d.Q) return;
-    const int64_t off = q * d.P + p;
-    if (p + 128 <= d.P && d.P % 8 == 0) {
-        if (d.out_bf16) {
-            uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(d.out) + off);
+__device__ __forceinline__ void add_scaled2(const uint32_t* v, uint64_t scale, float* acc) {
+    const float2 r = unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(v[0]), __uint_as_float(v[1])), scale,
+                                            pack_f32x2(acc[0], acc[1])));
+    acc[0] = r.x;
+    acc[1] = r.y;
+}
+
+// The sums of a warp's 32 rows (one per lane) x kCols columns -> out.
+// A row's sums sit in one thread, so storing them from there would write 32 scattered pieces
+// per instruction; they are turned in shared memory (64 bytes of every row at a time, 16-byte
+// chunks swizzled so that neither side has bank conflicts) and leave as runs of 64 bytes.
+template <typename T>
+__device__ __forceinline__ void store_rows(const Fp8Product& d, int64_t q, int64_t p, const float (&acc)[kCols],
+                                           uint8_t* turn, int lane) {
+    constexpr int kPer = 64 / static_cast<int>(sizeof(T));  // columns per round: 16 or 32
+    const bool wide = (d.P * static_cast<int64_t>(sizeof(T))) % 16 == 0;
+    T* out = static_cast<T*>(d.out);
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-                o[j] = make_uint4(pack_bf16(unpack_f32x2(acc[4 * j])), pack_bf16(unpack_f32x2(acc[4 * j + 1])),
-                                  pack_bf16(unpack_f32x2(acc[4 * j + 2])), pack_bf16(unpack_f32x2(acc[4 * j + 3])));
+    for (int c0 = 0; c0 < kCols; c0 += kPer) {
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            uint4 w;
+            if constexpr (sizeof(T) == 2) {
+                const float* s = &acc[c0 + 8 * c];
+                w = make_uint4(pack_bf16(s[0], s[1]), pack_bf16(s[2], s[3]), pack_bf16(s[4], s[5]),
+                               pack_bf16(s[6], s[7]));
+            } else {
+                const float* s = &acc[c0 + 4 * c];
+                w = make_uint4(__float_as_uint(s[0]), __float_as_uint(s[1]), __float_as_uint(s[2]),
+                               __float_as_uint(s[3]));
+            }
+            *reinterpret_cast<uint4*>(turn + 64 * lane + ((c ^ ((lane >> 1) & 3)) << 4)) = w;
+        }
+        __syncwarp();
+        if (wide) {
+            const int64_t pc = p + c0 + (lane & 3) * (16 / static_cast<int>(sizeof(T)));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = 8 * i + (lane >> 2);
+                const uint4 w = *reinterpret_cast<const uint4*>(turn + 64 * r + (((lane & 3) ^ ((r >> 1) & 3)) << 4));
+                if (q + r < d.Q && pc < d.P) *reinterpret_cast<uint4*>(out + (q + r) * d.P + pc) = w;
+            }
         } else {
-            float4* o = reinterpret_cast<float4*>(static_cast<float*>(d.out) + off);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-                const float2 a = unpack_f32x2(acc[2 * j]), b = unpack_f32x2(acc[2 * j + 1]);
-                o[j] = make_float4(a.x, a.y, b.x, b.y);
+            // rows of `out` start anywhere: neighbouring lanes store neighbouring elements
+            for (int e = lane; e < 32 * kPer; e += 32) {
+                const int r = e / kPer, c = e % kPer;
+                const int byte = c * static_cast<int>(sizeof(T));
+                const T v = *reinterpret_cast<const T*>(turn + 64 * r + (((byte >> 4) ^ ((r >> 1) & 3)) << 4) + (byte & 15));
+                if (q + r < d.Q && p + c0 + c < d.P) out[(q + r) * d.P + p + c0 + c] = v;
             }
         }
-        return;
-    }
-#pragma unroll
-    for (int j = 0; j < 128; ++j) {
-        if (p + j >= d.P) break;
-        const float2 two = unpack_f32x2(acc[j / 2]);
-        const float y = j % 2 == 0 ? two.x : two.y;
-        if (d.out_bf16)
-            static_cast<__nv_bfloat16*>(d.out)[off + j] = __float2bfloat16_rn(y);
-        else
-            static_cast<float*>(d.out)[off + j] = y;
     }
 }
 
@@ -126,7 +158,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* gbase = smem_raw + (base - raw);
     const uint32_t sQ = base;
     const uint32_t sP = sQ + ST * kOpBytes;
-    const uint32_t sScale = sP + ST * kOpBytes;
+    const uint32_t sTurn = sP + ST * kOpBytes;
+    const uint32_t sScale = sTurn + kEpiWarps * kTurnBytes;
     const uint32_t sBar = sScale + kSlots * kSlotFloats * 4;
     auto full = [&](int s) { return sBar + 8u * s; };               // even CTA: both CTAs' loads
     auto empty = [&](int s) { return sBar + 8u * (ST + s); };       // local: stage read by the MMAs
@@ -176,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp < kWarpEpi) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsSmall));
-        if (warp == kWarpTma && lane == 0) {
+        if (warp == kWarpTma) {
             // ------------------------------------------------------------ producer --
             int stage = 0;
             uint32_t phase = 0;
@@ -192,10 +225,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ok = false;
                         break;
                     }
-                    if (leader) mbar_arrive_expect_tx(full(stage), 4 * kOpBytes);
-                    const uint32_t bar = mapa_shared(full(stage), 0);
-                    tma_load_2d_pair(sQ + stage * kOpBytes, &tmap_q, bar, g * kG, qr);
-                    tma_load_2d_pair(sP + stage * kOpBytes, &tmap_p, bar, g * kG, pr);
+                    if (elect_one()) {
+                        if (leader) mbar_arrive_expect_tx(full(stage), 4 * kOpBytes);
+                        const uint32_t bar = mapa_shared(full(stage), 0);
+                        tma_load_2d_pair(sQ + stage * kOpBytes, &tmap_q, bar, g * kG, qr);
+                        tma_load_2d_pair(sP + stage * kOpBytes, &tmap_p, bar, g * kG, pr);
+                    }
+                    __syncwarp();
                     ++issued;
                     if (++stage == ST) {
                         stage = 0;
@@ -209,41 +245,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const long long fills = (issued - s + ST - 1) / ST;
                     if (fills > 0) drain_wait(full(s), static_cast<uint32_t>((fills - 1) & 1));
                 }
-            }
-        } else if (warp == kWarpMma && lane == 0 && leader) {
-            // ---------------------------------------------------------- MMA issuer --
-            constexpr uint32_t idesc = idesc_e4m3(kTile, kTile);
-            int stage = 0, buf = 0;
-            uint32_t phase = 0, bphase = 0;
-            bool ok = true;
-            for (int tile = first; ok && tile < a.num_tiles; tile += step) {
-                for (int g = 0; g < a.groups; ++g) {
-                    if (!mbar_wait_cluster_bounded(tempty(buf), bphase ^ 1u, abort_flag) ||
-                        !mbar_wait_cluster_bounded(full(stage), phase, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t qa = sQ + stage * kOpBytes, pa = sP + stage * kOpBytes;
-#pragma unroll
-                    for (int kk = 0; kk < kG / 32; ++kk)
-                        tc_mma_f8_pair(tmem_base + static_cast<uint32_t>(buf * kTile), smem_desc_sw128(qa + kk * 32),
-                                       smem_desc_sw128(pa + kk * 32), idesc, kk != 0 ? 1u : 0u);
-                    tc_commit_pair_multicast(empty(stage), 0x3);
-                    tc_commit_pair_multicast(tfull(buf), 0x3);
-                    if (++stage == ST) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
-                    if (++buf == 2) {
-                        buf = 0;
-                        bphase ^= 1u;
-                    }
-                }
-            }
-            if (!ok) {
-                tc_commit_pair_multicast(drain_bar, 0x1);
-                drain_wait(drain_bar, 0);
             }
         } else if (warp == kWarpScale) {
             // -------------------------------------------------------------- scales --
@@ -260,19 +261,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ok = false;
                         break;
                     }
-                    const uint32_t dst = sScale + static_cast<uint32_t>(slot * kSlotFloats * 4);
+                    const uint32_t dst = sScale + static_cast<uint32_t>(slot * kSlotFloats * 4 + 4 * lane);
+                    const float* sq = a.d.sq + g * a.d.Q;
 #pragma unroll
-                    for (int c = 0; c < kHalf; c += 32) {
-                        const int64_t q = q0 + c + lane < a.d.Q ? q0 + c + lane : a.d.Q - 1;
-                        cp_async4(dst + 4u * (c + lane), a.d.sq + g * a.d.Q + q);
+                    for (int c = 0; c < kHalf / 32; ++c) {
+                        const int64_t q = q0 + 32 * c + lane;
+                        cp_async4(dst + 128u * c, sq + (q < a.d.Q ? q : a.d.Q - 1));
                     }
+                    const float* sp = a.d.sp + g * a.d.sp_g;
 #pragma unroll
-                    for (int c = 0; c < (ROWS ? kTile : 32); c += 32) {
+                    for (int c = 0; c < (ROWS ? kTile / 32 : 1); ++c) {
                         // by blocks: two of them, copied by lanes 0 and 1
                         if (!ROWS && lane > 1) break;
-                        const int64_t row = p0 + (ROWS ? c + lane : kHalf * lane);
+                        const int64_t row = p0 + (ROWS ? 32 * c + lane : kHalf * lane);
                         const int64_t p = row < a.d.P ? row : a.d.P - 1;
-                        cp_async4(dst + 4u * (kHalf + c + lane), a.d.sp + (p >> a.d.p_shift) * a.d.sp_p + g * a.d.sp_g);
+                        cp_async4(dst + 4u * kHalf + 128u * c, sp + (p >> a.d.p_shift) * a.d.sp_p);
                     }
                     cp_async_arrive(sfull(slot));
                     if (++slot == kSlots) {
@@ -282,58 +285,106 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             cp_async_wait_all();
+        } else if (warp == kWarpMma && leader) {
+            // ---------------------------------------------------------- MMA issuer --
+            constexpr uint32_t idesc = idesc_e4m3(kTile, kTile);
+            int stage = 0, buf = 0;
+            uint32_t phase = 0, bphase = 0;
+            bool ok = true;
+            for (int tile = first; ok && tile < a.num_tiles; tile += step) {
+                for (int g = 0; g < a.groups; ++g) {
+                    if (!mbar_wait_cluster_bounded(full(stage), phase, abort_flag) ||
+                        !mbar_wait_cluster_bounded(tempty(buf), bphase ^ 1u, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint32_t qa = sQ + stage * kOpBytes, pa = sP + stage * kOpBytes;
+#pragma unroll
+                        for (int kk = 0; kk < kG / 32; ++kk)
+                            tc_mma_f8_pair(tmem_base + static_cast<uint32_t>(buf * kTile),
+                                           smem_desc_sw128(qa + kk * 32), smem_desc_sw128(pa + kk * 32), idesc,
+                                           kk != 0 ? 1u : 0u);
+                        // the accumulator's readers are the ones being waited for
+                        tc_commit_pair_multicast(tfull(buf), 0x3);
+                        tc_commit_pair_multicast(empty(stage), 0x3);
+                    }
+                    __syncwarp();
+                    if (++stage == ST) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                    if (++buf == 2) {
+                        buf = 0;
+                        bphase ^= 1u;
+                    }
+                }
+            }
+            if (!ok) {
+                if (elect_one()) tc_commit_pair_multicast(drain_bar, 0x1);
+                __syncwarp();
+                drain_wait(drain_bar, 0);
+            }
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEpi));
         // ------------------------------------------------------------ epilogue --
-        const int quarter = warp & 3, half = (warp - kWarpEpi) >> 2;
+        // a thread: one row (its TMEM lane), kCols columns; sums by blocks use plain multiply-adds,
+        // which measured faster there than packed ones (8192^3: 586 against 650 us without stores)
+        const int quarter = warp & 3, block = (warp - kWarpEpi) >> 2;
         const int r = 32 * quarter + lane;
-        const uint32_t t_addr = tmem_base + (static_cast<uint32_t>(32 * quarter) << 16) + 128u * half;
+        const uint32_t t_addr =
+            tmem_base + (static_cast<uint32_t>(32 * quarter) << 16) + static_cast<uint32_t>(kCols * block);
+        uint8_t* turn = gbase + (sTurn - base) + (warp - kWarpEpi) * kTurnBytes;
         int slot = 0, buf = 0;
         uint32_t sphase = 0, bphase = 0;
         bool ok = true;
         for (int tile = first; tile < a.num_tiles; tile += step) {
-            int64_t q0, p0;
-            tile_origin(a, tile, q0, p0);
-            uint64_t acc[64];
+            float acc[kCols];
 #pragma unroll
-            for (int j = 0; j < 64; ++j) acc[j] = 0;
+            for (int j = 0; j < kCols; ++j) acc[j] = 0.0f;
             for (int g = 0; g < a.groups; ++g) {
-                if (!mbar_wait_bounded(sfull(slot), sphase, abort_flag) ||
-                    !mbar_wait_cluster_bounded(tfull(buf), bphase, abort_flag)) {
+                if (!mbar_wait_bounded(sfull(slot), sphase, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                const float* sc = scales + slot * kSlotFloats;
+                const float fq = sc[r] * (ROWS ? 1.0f : sc[kHalf + block * kCols / kHalf]);
+                if (!mbar_wait_cluster_bounded(tfull(buf), bphase, abort_flag)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const float* sc = scales + slot * kSlotFloats;
-                const float fq = sc[r] * (ROWS ? 1.0f : sc[kHalf + half]);
-                const uint64_t f2 = pack_f32x2(fq, fq);
                 const uint32_t addr = t_addr + static_cast<uint32_t>(buf * kTile);
-                uint32_t v[2][32];
-                tmem_ld_32x32b_x32(addr, v[0]);
+                // the next 32 columns are on their way while these are scaled
+                uint32_t v2[2][32];
+                tmem_ld_32x32b_x32(addr, v2[0]);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    tmem_ld_wait_for(v[c & 1]);
-                    if (c < 3) {
-                        tmem_ld_32x32b_x32(addr + 32u * (c + 1), v[(c + 1) & 1]);
+                for (int c = 0; c < kCols / 32; ++c) {
+                    uint32_t(&v)[32] = v2[c & 1];
+                    tmem_ld_wait_for(v);
+                    if (c + 1 < kCols / 32) {
+                        tmem_ld_32x32b_x32(addr + 32u * (c + 1), v2[(c + 1) & 1]);
                     } else {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive_cluster(mapa_shared(tempty(buf), 0));
                     }
-                    const float4* sp4 = reinterpret_cast<const float4*>(sc + kHalf + 128 * half + 32 * c);
+                    float* o = &acc[32 * c];
+                    if constexpr (ROWS) {
+                        // two scales per sum: packed arithmetic halves the instructions
+                        const float4* sp4 = reinterpret_cast<const float4*>(sc + kHalf + kCols * block + 32 * c);
+                        const uint64_t f2 = pack_f32x2(fq, fq);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const uint32_t* w = &v[c & 1][4 * j];
-                        uint64_t lo = f2, hi = f2;
-                        if constexpr (ROWS) {
+                        for (int j = 0; j < 8; ++j) {
                             const float4 s4 = sp4[j];
-                            lo = mul_f32x2(f2, pack_f32x2(s4.x, s4.y));
-                            hi = mul_f32x2(f2, pack_f32x2(s4.z, s4.w));
+                            add_scaled2(v + 4 * j, mul_f32x2(f2, pack_f32x2(s4.x, s4.y)), o + 4 * j);
+                            add_scaled2(v + 4 * j + 2, mul_f32x2(f2, pack_f32x2(s4.z, s4.w)), o + 4 * j + 2);
                         }
-                        uint64_t* o = &acc[16 * c + 2 * j];
-                        o[0] = fma_f32x2(pack_f32x2(__uint_as_float(w[0]), __uint_as_float(w[1])), lo, o[0]);
-                        o[1] = fma_f32x2(pack_f32x2(__uint_as_float(w[2]), __uint_as_float(w[3])), hi, o[1]);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) o[j] = fmaf(__uint_as_float(v[j]), fq, o[j]);
                     }
                 }
                 __syncwarp();
@@ -348,7 +399,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (!ok) break;
-            store_row(a.d, q0 + kHalf * static_cast<int>(rank) + r, p0 + 128 * half, acc);
+            int64_t q0, p0;
+            tile_origin(a, tile, q0, p0);
+            q0 += kHalf * static_cast<int>(rank) + 32 * quarter;
+            p0 += kCols * block;
+            if (a.d.out_bf16)
+                store_rows<__nv_bfloat16>(a.d, q0, p0, acc, turn, lane);
+            else
+                store_rows<float>(a.d, q0, p0, acc, turn, lane);
         }
     }
 
