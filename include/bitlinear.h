@@ -421,11 +421,13 @@ BL_API size_t bitlinear_norm_backward_workspace_size(int64_t M, int64_t K);
  *   ws, ws_bytes    : device workspace of at least bitlinear_norm_backward_workspace_size
  *                     bytes, scratch for the duration of the enqueued work (calls that may
  *                     run at the same time need one each).
+ *   err_word    out : optional; BL_ERRBIT_TIMEOUT if a bounded device wait gave up (the
+ *                     outputs are then incomplete).
  * Errors: as the forward, and BL_ERR_WORKSPACE. */
 BL_API bl_status bitlinear_norm_backward(const void *dY, bl_dtype dy_dtype, const void *X, bl_dtype x_dtype,
                                          const float *norm_weight, int64_t M, int64_t K, bl_norm_kind norm_kind,
                                          float norm_eps, void *dX, bl_dtype dx_dtype, float *dweight, float *dbias,
-                                         void *ws, size_t ws_bytes, void *stream);
+                                         void *ws, size_t ws_bytes, int32_t *err_word, void *stream);
 
 /* ----------------------------------------------------------------------------------
  * 8-bit floating-point product with a scale for each block of 128, for the layers of a

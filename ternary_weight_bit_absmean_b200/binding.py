@@ -108,7 +108,7 @@ def lib() -> ctypes.CDLL:
         L.bitlinear_norm_forward.restype = S
         L.bitlinear_norm_backward_workspace_size.argtypes = [I64, I64]
         L.bitlinear_norm_backward_workspace_size.restype = ctypes.c_size_t
-        L.bitlinear_norm_backward.argtypes = [P, S, P, S, P, I64, I64, S, F, P, S, P, P, P, ctypes.c_size_t, P]
+        L.bitlinear_norm_backward.argtypes = [P, S, P, S, P, I64, I64, S, F, P, S, P, P, P, ctypes.c_size_t, P, P]
         L.bitlinear_norm_backward.restype = S
         L.bitlinear_fp8_row_bytes.argtypes = [I64]
         L.bitlinear_fp8_row_bytes.restype = I64
@@ -370,13 +370,14 @@ def bitlinear_norm_backward_workspace_size(M: int, K: int) -> int:
     return int(lib().bitlinear_norm_backward_workspace_size(int(M), int(K)))
 
 
-def bitlinear_norm_backward(dY, X, norm_weight, kind, norm_eps, dX, dweight, dbias, ws, stream=None):
+def bitlinear_norm_backward(dY, X, norm_weight, kind, norm_eps, dX, dweight, dbias, ws, err_word=None, stream=None):
     M, K = _matrix(X, "X")
-    with _scope(stream, X, dY, norm_weight, dX, dweight, dbias, ws):
+    with _scope(stream, X, dY, norm_weight, dX, dweight, dbias, ws, err_word):
         _check(lib().bitlinear_norm_backward(
             *_float(dY, "dY", (M, K)), *_float(X, "X"), _vec(norm_weight, "norm_weight", K), M, K, int(kind),
             float(norm_eps), *_float(dX, "dX", (M, K)), _vec(dweight, "dweight", K), _vec(dbias, "dbias", K),
-            None if ws is None else _dev(ws, torch.uint8, "ws"), 0 if ws is None else ws.numel(), _stream(None)),
+            None if ws is None else _dev(ws, torch.uint8, "ws"), 0 if ws is None else ws.numel(),
+            _opt(err_word, "err_word"), _stream(None)),
             "bitlinear_norm_backward")
 
 
@@ -528,7 +529,7 @@ def norm_forward(X: torch.Tensor, norm_weight=None, norm_bias=None, kind=BL_NORM
 
 
 def norm_backward(dY: torch.Tensor, X: torch.Tensor, norm_weight=None, kind=BL_NORM_RMS, norm_eps: float = 1e-5,
-                  bias: bool = False, dx_dtype=None, stream=None):
+                  bias: bool = False, dx_dtype=None, stream=None, err_word=None):
     """(dX [M, K], dweight [K] fp32, dbias [K] fp32) of norm_forward for the gradient dY at its
     result.  dX is dx_dtype (dY's type by default); dweight is None without a norm_weight,
     dbias unless `bias`."""
@@ -539,7 +540,7 @@ def norm_backward(dY: torch.Tensor, X: torch.Tensor, norm_weight=None, kind=BL_N
         db = torch.empty(K, dtype=torch.float32, device=X.device) if bias else None
         n = bitlinear_norm_backward_workspace_size(M, K)
         ws = torch.empty(n, dtype=torch.uint8, device=X.device) if n else None
-        bitlinear_norm_backward(dY, X, norm_weight, kind, norm_eps, dX, dw, db, ws)
+        bitlinear_norm_backward(dY, X, norm_weight, kind, norm_eps, dX, dw, db, ws, err_word)
     return dX, dw, db
 
 

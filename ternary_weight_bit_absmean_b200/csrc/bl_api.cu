@@ -386,7 +386,7 @@ size_t bitlinear_norm_backward_workspace_size(int64_t M, int64_t K) {
 bl_status bitlinear_norm_backward(const void* dY, bl_dtype dy_dtype, const void* X, bl_dtype x_dtype,
                                   const float* norm_weight, int64_t M, int64_t K, bl_norm_kind norm_kind,
                                   float norm_eps, void* dX, bl_dtype dx_dtype, float* dweight, float* dbias, void* ws,
-                                  size_t ws_bytes, void* stream) {
+                                  size_t ws_bytes, int32_t* err_word, void* stream) {
     BL_RANGE("bitlinear_norm_backward");
     if (dY == nullptr || X == nullptr || dX == nullptr) return BL_ERR_INVALID_ARG;
     if (!float_dtype(dy_dtype) || !float_dtype(x_dtype) || !float_dtype(dx_dtype)) return BL_ERR_INVALID_ARG;
@@ -402,7 +402,7 @@ bl_status bitlinear_norm_backward(const void* dY, bl_dtype dy_dtype, const void*
     if (!aligned16(ws)) return BL_ERR_MISALIGNED;
     return cuda_status(bl::launch_norm_backward(dY, dy_dtype == BL_OUT_BF16, X, x_dtype == BL_OUT_BF16, norm_weight, M,
                                                 K, static_cast<int>(norm_kind), norm_eps, dX, dx_dtype == BL_OUT_BF16,
-                                                dweight, dbias, ws, as_stream(stream)));
+                                                dweight, dbias, ws, err_word, as_stream(stream)));
 }
 
 int64_t bitlinear_fp8_row_bytes(int64_t K) { return K <= 0 ? 0 : bl::fp8_row_bytes(K); }

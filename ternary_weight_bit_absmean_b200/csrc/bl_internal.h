@@ -140,7 +140,7 @@ cudaError_t launch_norm_forward(const void* X, bool x_bf16, const float* w, cons
 size_t norm_backward_workspace(int64_t M, int64_t K);
 cudaError_t launch_norm_backward(const void* dY, bool dy_bf16, const void* X, bool x_bf16, const float* w, int64_t M,
                                  int64_t K, int kind, float eps, void* dX, bool dx_bf16, float* dw, float* db,
-                                 void* ws, cudaStream_t stream);
+                                 void* ws, int32_t* err, cudaStream_t stream);
 
 // e4m3 codes with one scale per block of 128 (k_fp8_quant.cu): rows of codes are
 // fp8_row_bytes(K) apart.  Activations: codes and scales along rows (q, s) and / or along

@@ -16,12 +16,23 @@
 // of a row add in a tree, and the squares are of the already centred values, so a large
 // mean costs no digits.
 //
-// Both are bound by memory (a row is read once, kept in registers, and written once).
-// `TPR` threads hold a row, up to CH chunks of eight elements each; short rows share a
-// block.  The column sums of the backward stay in the registers of the threads that own
-// the columns while a block walks over its rows; they are added over the row groups of a
-// block in shared memory and over the blocks by a second kernel, always in the same
-// order, so the results do not change from run to run.
+// Both are bound by memory: a row is read once, held in registers as it came, and written once.
+// A matrix is cut into chunks of eight elements of its flat order, whatever K is, so that every
+// access is 16 bytes wide on 16-byte boundaries in each of the matrices; a row's first and last
+// chunk may belong to its neighbours in part, and those elements are masked.
+//
+// Forward: many small blocks, each thread one to four chunks of a row; the blocks on an SM
+// overlap one another's loads, sums and stores.
+// Backward: the threads of a row also keep the sums of their columns, which fills the register
+// file with one resident block.  There a ring of rows in shared memory, filled by one warp with
+// bulk copies, keeps the memory busy meanwhile.  Short rows share the block between groups of
+// threads.  Rows of more than kSlice columns are split over a cluster of blocks that exchange
+// their row sums through distributed shared memory.
+//
+// The column sums of the backward stay in the registers of the threads that own the columns
+// while a block walks over its rows; they are added over the rows of a block in shared memory
+// and over the blocks by a second kernel, always in the same order, so the results do not
+// change from run to run.
 #include <cuda_bf16.h>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -32,128 +43,150 @@
 namespace bl {
 namespace {
 
-constexpr int kE = 8;  // elements of a chunk
+constexpr int kE = 8;            // elements of a chunk
+constexpr int kSlice = 9712;     // most columns of a block of the backward
+constexpr int kMaxCluster = 8;
+constexpr int kMaxGroups = 24;   // groups of threads of a block
+constexpr int kMaxThreads = 1024;
+constexpr int kMaxStages = 8;
+constexpr int kRingBytes = 208 * 1024;
+constexpr int kParts = 148;      // most blocks or clusters: one per SM
+constexpr unsigned long long kDrainNs = 200000000ull;
 
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
-
-// Element e of chunk c of a thread sits at row offset elem<VEC>(c, e): eight neighbours per
-// chunk when the rows are 16-byte aligned (K % 8 == 0), else neighbouring threads hold
-// neighbouring elements so that single-element accesses still coalesce.
-template <bool VEC>
-__device__ __forceinline__ int64_t elem(int c, int e, int t, int tpr) {
-    const int64_t chunk = static_cast<int64_t>(c) * tpr;
-    return VEC ? (chunk + t) * kE + e : (chunk * kE + static_cast<int64_t>(e) * tpr + t);
-}
-
-template <bool VEC>
-__device__ __forceinline__ void load_chunk(const float* row, int c, int t, int tpr, int64_t K, float (&v)[kE]) {
-    if constexpr (VEC) {
-        const int64_t k = elem<true>(c, 0, t, tpr);
-        if (k < K) {
-            const float4 a = __ldg(reinterpret_cast<const float4*>(row + k));
-            const float4 b = __ldg(reinterpret_cast<const float4*>(row + k + 4));
-            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-            v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-        } else {
-#pragma unroll
-            for (int e = 0; e < kE; ++e) v[e] = 0.0f;
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < kE; ++e) {
-            const int64_t k = elem<false>(c, e, t, tpr);
-            v[e] = k < K ? __ldg(row + k) : 0.0f;
-        }
-    }
-}
-
-template <bool VEC>
-__device__ __forceinline__ void load_chunk(const __nv_bfloat16* row, int c, int t, int tpr, int64_t K,
-                                           float (&v)[kE]) {
-    if constexpr (VEC) {
-        const int64_t k = elem<true>(c, 0, t, tpr);
-        uint4 a = make_uint4(0, 0, 0, 0);
-        if (k < K) a = __ldg(reinterpret_cast<const uint4*>(row + k));
-        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(w[i] << 16);
-            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < kE; ++e) {
-            const int64_t k = elem<false>(c, e, t, tpr);
-            v[e] = k < K ? __bfloat162float(row[k]) : 0.0f;
-        }
-    }
-}
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&p);
 }
 
-// One chunk of a row of `out` (fp32 or bf16 by `bf16`).
-template <bool VEC>
-__device__ __forceinline__ void store_chunk(void* out, bool bf16, int64_t row_off, int c, int t, int tpr, int64_t K,
-                                            const float (&v)[kE]) {
-    if constexpr (VEC) {
-        const int64_t k = elem<true>(c, 0, t, tpr);
-        if (k >= K) return;
+// A chunk as it lies in memory, and its values.
+template <typename T>
+struct Raw;
+template <>
+struct Raw<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float* p) {
+        a = *reinterpret_cast<const float4*>(p);
+        b = *reinterpret_cast<const float4*>(p + 4);
+    }
+    __device__ __forceinline__ void load_global(const float* p) {
+        a = __ldg(reinterpret_cast<const float4*>(p));
+        b = __ldg(reinterpret_cast<const float4*>(p + 4));
+    }
+    __device__ __forceinline__ void clear() { a = b = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
+    __device__ __forceinline__ float operator[](int e) const {
+        switch (e) {
+            case 0: return a.x;
+            case 1: return a.y;
+            case 2: return a.z;
+            case 3: return a.w;
+            case 4: return b.x;
+            case 5: return b.y;
+            case 6: return b.z;
+            default: return b.w;
+        }
+    }
+};
+template <>
+struct Raw<__nv_bfloat16> {
+    uint4 a;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = *reinterpret_cast<const uint4*>(p); }
+    __device__ __forceinline__ void load_global(const __nv_bfloat16* p) {
+        a = __ldg(reinterpret_cast<const uint4*>(p));
+    }
+    __device__ __forceinline__ void clear() { a = make_uint4(0u, 0u, 0u, 0u); }
+    __device__ __forceinline__ float operator[](int e) const {
+        const uint32_t w = e < 2 ? a.x : e < 4 ? a.y : e < 6 ? a.z : a.w;
+        return __uint_as_float((e & 1) ? (w & 0xFFFF0000u) : (w << 16));
+    }
+};
+
+// The elements [lo, hi) of a chunk that belong to the row (all eight where rows are whole
+// chunks).
+struct Mask {
+    int lo, hi;
+    __device__ __forceinline__ bool any() const { return lo < hi; }
+    __device__ __forceinline__ bool all() const { return lo <= 0 && hi >= kE; }
+    __device__ __forceinline__ bool has(int e) const { return e >= lo && e < hi; }
+};
+
+// A chunk of the matrix at flat element `flat` (a multiple of eight) from global memory: one
+// access if it lies inside the matrix of `total` elements, else element by element (only the
+// matrix's last chunk).
+template <typename T>
+__device__ __forceinline__ void load_flat(const T* base, int64_t flat, int64_t total, float (&v)[kE]) {
+#pragma unroll
+    for (int e = 0; e < kE; ++e) v[e] = flat + e < total ? to_f32(base[flat + e]) : 0.0f;
+}
+
+// A chunk of the output at flat element `flat`, as fp32 or bf16.
+__device__ __forceinline__ void store_flat(void* out, bool bf16, int64_t flat, const Mask& m, const float (&v)[kE]) {
+    if (m.all()) {
         if (bf16) {
-            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out) + row_off + k) =
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out) + flat) =
                 make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
         } else {
-            float4* p = reinterpret_cast<float4*>(static_cast<float*>(out) + row_off + k);
+            float4* p = reinterpret_cast<float4*>(static_cast<float*>(out) + flat);
             p[0] = make_float4(v[0], v[1], v[2], v[3]);
             p[1] = make_float4(v[4], v[5], v[6], v[7]);
         }
-    } else {
+        return;
+    }
 #pragma unroll
-        for (int e = 0; e < kE; ++e) {
-            const int64_t k = elem<false>(c, e, t, tpr);
-            if (k >= K) continue;
-            if (bf16)
-                static_cast<__nv_bfloat16*>(out)[row_off + k] = __float2bfloat16_rn(v[e]);
-            else
-                static_cast<float*>(out)[row_off + k] = v[e];
-        }
+    for (int e = 0; e < kE; ++e) {
+        if (!m.has(e)) continue;
+        if (bf16)
+            static_cast<__nv_bfloat16*>(out)[flat + e] = __float2bfloat16_rn(v[e]);
+        else
+            static_cast<float*>(out)[flat + e] = v[e];
     }
 }
 
-// Sums of two values over the TPR threads of a row (TPR a multiple of 32; the group's
-// threads call it together).  `slot` alternates between calls: a slot is written again
-// only after the barrier of the call in between, which every reader has then passed.
-struct RowSum {
-    float2* buf;  // [2][32] of this row group
+// Eight values of a vector over k from column k (which may be masked or unaligned).
+template <bool EDGE>
+__device__ __forceinline__ void load_vector(const float* p, float fill, int64_t k, const Mask& m, float (&v)[kE]) {
+    if (!EDGE && p != nullptr && m.any()) {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(p + k)), b = __ldg(reinterpret_cast<const float4*>(p + k + 4));
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+        v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < kE; ++e) v[e] = p != nullptr && m.has(e) ? __ldg(p + k + e) : fill;
+}
+
+// Sums of two values over the threads of a group.  Slots alternate between calls: one is
+// written again only after a barrier that every reader of it has passed.
+struct GroupSum {
+    float2* buf;  // [2][32] of this group
     int t, tpr, group;
-    int slot = 0;
+    uint32_t calls = 0;
     __device__ __forceinline__ float2 operator()(float a, float b) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
             a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
             b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
         }
-        if (tpr == 32) return make_float2(a, b);
-        float2* s = buf + 32 * slot;
-        slot ^= 1;
-        if ((t & 31) == 0) s[t >> 5] = make_float2(a, b);
-        asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(tpr) : "memory");
-        const float2 v = (t & 31) < (tpr >> 5) ? s[t & 31] : make_float2(0.0f, 0.0f);
-        a = v.x, b = v.y;
+        if (tpr > 32) {
+            float2* s = buf + 32 * (calls & 1);
+            if ((t & 31) == 0) s[t >> 5] = make_float2(a, b);
+            asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(tpr) : "memory");
+            const float2 v = (t & 31) < (tpr >> 5) ? s[t & 31] : make_float2(0.0f, 0.0f);
+            a = v.x, b = v.y;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
-            b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
+            for (int o = 16; o > 0; o >>= 1) {
+                a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+                b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
+            }
         }
+        ++calls;
         return make_float2(a, b);
     }
 };
 
-constexpr int kMaxGroups = 8;   // row groups of a block
-constexpr int kMaxThreads = 1024;
+// -------------------------------------------------------------------------- forward --
 
 struct FwdArgs {
     const float* w;
@@ -165,62 +198,129 @@ struct FwdArgs {
     bool out_bf16;
 };
 
-template <typename TX, bool VEC, int CH>
-__global__ void __launch_bounds__(kMaxThreads) norm_forward_kernel(const TX* __restrict__ X, const FwdArgs a) {
-    __shared__ float2 sums[kMaxGroups][64];
+// block: x = threads of a row, y = rows.  EDGE: rows are not whole chunks.
+template <typename TX, bool EDGE, int CH, int THREADS, int BLOCKS>
+__global__ void __launch_bounds__(THREADS, BLOCKS) norm_forward_kernel(const TX* __restrict__ X, const FwdArgs a) {
+    __shared__ float2 sums[8][64];
     const int t = threadIdx.x, tpr = blockDim.x, group = threadIdx.y;
     pdl_wait_then_release();
-    RowSum row_sum{sums[group], t, tpr, group};
+    GroupSum row_sum{sums[group], t, tpr, group};
     const int64_t m = static_cast<int64_t>(blockIdx.x) * blockDim.y + group;
     if (m >= a.M) return;  // a whole group leaves together
-    const TX* row = X + m * a.K;
-    float x[CH][kE];
+    const int64_t first = m * a.K;
+    const int skip = EDGE ? static_cast<int>(first & (kE - 1)) : 0;  // of the first chunk
+    const int64_t flat0 = first - skip;
+    auto mask = [&](int c) {
+        const int64_t k = static_cast<int64_t>(c * tpr + t) * kE - skip;  // column of the chunk's element 0
+        if constexpr (EDGE)
+            return Mask{k < 0 ? static_cast<int>(-k) : 0, a.K - k < kE ? static_cast<int>(a.K - k) : kE};
+        else
+            return Mask{0, k < a.K ? kE : 0};
+    };
+    Raw<TX> x[CH];
 #pragma unroll
-    for (int c = 0; c < CH; ++c) load_chunk<VEC>(row, c, t, tpr, a.K, x[c]);
+    for (int c = 0; c < CH; ++c) {
+        const int64_t flat = flat0 + static_cast<int64_t>(c * tpr + t) * kE;
+        if (mask(c).any() && (!EDGE || flat + kE <= a.M * a.K))
+            x[c].load_global(X + flat);
+        else
+            x[c].clear();
+    }
+    // the values of chunk c, zero where they are not the row's
+    auto values = [&](int c, float(&v)[kE]) {
+        if constexpr (EDGE) {
+            const int64_t flat = flat0 + static_cast<int64_t>(c * tpr + t) * kE;
+            const Mask k = mask(c);
+            if (k.any() && flat + kE > a.M * a.K) {
+                load_flat(X, flat, a.M * a.K, v);  // the matrix's last chunk
+            } else {
+#pragma unroll
+                for (int e = 0; e < kE; ++e) v[e] = x[c][e];
+            }
+            if (!k.all())
+#pragma unroll
+                for (int e = 0; e < kE; ++e)
+                    if (!k.has(e)) v[e] = 0.0f;
+        } else {
+#pragma unroll
+            for (int e = 0; e < kE; ++e) v[e] = x[c][e];
+        }
+    };
     float mu = 0.0f;
     if (a.layer) {
         float s = 0.0f;
 #pragma unroll
-        for (int c = 0; c < CH; ++c)
+        for (int c = 0; c < CH; ++c) {
+            float v[kE];
+            values(c, v);
 #pragma unroll
-            for (int e = 0; e < kE; ++e) s += x[c][e];
+            for (int e = 0; e < kE; ++e) s += v[e];
+        }
         mu = row_sum(s, 0.0f).x * a.inv_k;
     }
-    float v = 0.0f;
-#pragma unroll
-    for (int c = 0; c < CH; ++c)
-#pragma unroll
-        for (int e = 0; e < kE; ++e) {
-            if (elem<VEC>(c, e, t, tpr) < a.K) {
-                x[c][e] -= mu;
-                v = fmaf(x[c][e], x[c][e], v);
-            }
-        }
-    const float r = 1.0f / sqrtf(row_sum(v, 0.0f).x * a.inv_k + a.eps);
+    float q = 0.0f;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-        float w[kE], b[kE];
-        if (a.w != nullptr) load_chunk<VEC>(a.w, c, t, tpr, a.K, w);
-        if (a.b != nullptr) load_chunk<VEC>(a.b, c, t, tpr, a.K, b);
+        const Mask k = mask(c);
+        if (!k.any()) continue;
+        float v[kE];
+        values(c, v);
 #pragma unroll
         for (int e = 0; e < kE; ++e) {
-            float y = x[c][e] * r;
-            if (a.w != nullptr) y *= w[e];
-            if (a.b != nullptr) y += b[e];
-            x[c][e] = y;
+            const float z = !EDGE || k.has(e) ? v[e] - mu : 0.0f;
+            q = fmaf(z, z, q);
         }
-        store_chunk<VEC>(a.out, a.out_bf16, m * a.K, c, t, tpr, a.K, x[c]);
+    }
+    const float r = 1.0f / sqrtf(row_sum(q, 0.0f).x * a.inv_k + a.eps);
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+        const Mask k = mask(c);
+        if (!k.any()) continue;
+        const int64_t col = static_cast<int64_t>(c * tpr + t) * kE - skip;
+        float v[kE], w[kE], b[kE];
+        values(c, v);
+        load_vector<EDGE>(a.w, 1.0f, col, k, w);
+        load_vector<EDGE>(a.b, 0.0f, col, k, b);
+#pragma unroll
+        for (int e = 0; e < kE; ++e) v[e] = (v[e] - mu) * r * w[e] + b[e];
+        store_flat(a.out, a.out_bf16, flat0 + static_cast<int64_t>(c * tpr + t) * kE, k, v);
     }
 }
 
-// Rows too long for the registers of a block: three passes over the row (it stays in the
-// caches between them).
+// The two sums over a whole block, for rows too long for its registers.
+struct BlockSum {
+    float2* buf;  // [2][32]
+    int t, tpr;
+    int slot = 0;
+    __device__ __forceinline__ float2 operator()(float a, float b) {
+        float2* s = buf + 32 * slot;
+        slot ^= 1;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+            b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
+        }
+        if ((t & 31) == 0) s[t >> 5] = make_float2(a, b);
+        __syncthreads();
+        const float2 v = (t & 31) < (tpr >> 5) ? s[t & 31] : make_float2(0.0f, 0.0f);
+        a = v.x, b = v.y;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+            b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
+        }
+        return make_float2(a, b);
+    }
+};
+
+// Rows too long for the registers of a block: three passes over the row (it stays in the caches
+// between them).
 template <typename TX>
 __global__ void __launch_bounds__(kMaxThreads) norm_forward_long_kernel(const TX* __restrict__ X, const FwdArgs a) {
     __shared__ float2 sums[64];
     const int t = threadIdx.x, tpr = blockDim.x;
     pdl_wait_then_release();
-    RowSum row_sum{sums, t, tpr, 0};
+    BlockSum row_sum{sums, t, tpr};
     const int64_t m = blockIdx.x;
     const TX* row = X + m * a.K;
     float mu = 0.0f;
@@ -246,133 +346,362 @@ __global__ void __launch_bounds__(kMaxThreads) norm_forward_long_kernel(const TX
     }
 }
 
+// ------------------------------------------------- backward: the ring of rows --
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+        "l"(src), "r"(bytes), "r"(bar)
+        : "memory");
+}
+
+// What a block works on.  Group g of batch i takes row first + i * step + g; with rows that are
+// not whole chunks the number of rows in step is a multiple of eight, so that a group's rows
+// all start at the same place of a chunk and a thread's columns stay the same.
+struct Shape {
+    int64_t M, K;
+    int tpr, groups;     // threads of a row, rows at a time
+    int stages;
+    int slot_x, slot_d;  // bytes of a slot for x and for dy
+    int slice;           // columns of a block
+};
+
+struct Control {
+    uint64_t full[kMaxStages], empty[kMaxStages];
+    uint64_t cross[2];                    // row sums of the blocks of the cluster
+    float2 cross_sums[2][kMaxCluster];
+    float2 sums[kMaxGroups][64];
+    int abort;
+};
+
+// GroupSum, then over the blocks of the cluster (each sends its sums to all).  A slot is
+// written again only after the other blocks' next sums, sent by threads that have read it.
+struct RowSum {
+    GroupSum local;
+    Control* ctl;
+    int cluster;
+    uint32_t rank;
+    __device__ __forceinline__ float2 operator()(float a, float b) {
+        const uint32_t call = local.calls;
+        const float2 own = local(a, b);
+        if (cluster == 1) return own;
+        const int slot = static_cast<int>(call & 1), t = local.t;
+        const uint32_t bar = smem_u32(&ctl->cross[slot]);
+        if (t == 0) mbar_arrive_expect_tx(bar, 8u * static_cast<uint32_t>(cluster));
+        if (t < cluster) {
+            const uint32_t dst = mapa_shared(smem_u32(&ctl->cross_sums[slot][rank]), static_cast<uint32_t>(t));
+            const uint32_t rbar = mapa_shared(bar, static_cast<uint32_t>(t));
+            asm volatile(
+                "st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];" ::"r"(dst),
+                "r"(__float_as_uint(own.x)), "r"(__float_as_uint(own.y)), "r"(rbar)
+                : "memory");
+        }
+        mbar_wait_bounded(bar, (call >> 1) & 1u, &ctl->abort);
+        float2 all = make_float2(0.0f, 0.0f);
+        for (int i = 0; i < cluster; ++i) {
+            all.x += ctl->cross_sums[slot][i].x;
+            all.y += ctl->cross_sums[slot][i].y;
+        }
+        return all;
+    }
+};
+
+__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
+    const unsigned long long t0 = globaltimer_ns();
+    while (!mbar_try_wait(bar, parity)) {
+        if (globaltimer_ns() - t0 > kDrainNs) return;
+    }
+}
+
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+
+// Where a block stands.
+struct Place {
+    Control* ctl;
+    uint8_t* ring;
+    int t, group, tpr;
+    bool producer;
+    int cluster;
+    uint32_t rank;
+    int64_t first, step;  // its batches start at rows first, first + step, ...
+    int k0, ks;           // its columns
+    __device__ __forceinline__ Place(uint8_t* smem, const Shape& s) {
+        ctl = reinterpret_cast<Control*>(smem);
+        ring = smem + ((sizeof(Control) + 127) & ~size_t(127));
+        tpr = s.tpr;
+        producer = static_cast<int>(threadIdx.x) >= tpr * s.groups;
+        group = threadIdx.x / tpr;
+        t = threadIdx.x - group * tpr;
+        cluster = static_cast<int>(cluster_size());
+        rank = cluster_ctarank();
+        first = static_cast<int64_t>(blockIdx.x / cluster) * s.groups;
+        step = static_cast<int64_t>(gridDim.x / cluster) * s.groups;
+        k0 = static_cast<int>(rank) * s.slice;
+        ks = s.K - k0 < s.slice ? static_cast<int>(s.K - k0) : s.slice;
+        if (threadIdx.x == 0) {
+            for (int i = 0; i < s.stages; ++i) {
+                mbar_init(smem_u32(&ctl->full[i]), 1);
+                mbar_init(smem_u32(&ctl->empty[i]), tpr * s.groups / 32);
+            }
+            mbar_init(smem_u32(&ctl->cross[0]), 1);
+            mbar_init(smem_u32(&ctl->cross[1]), 1);
+            ctl->abort = 0;
+            mbar_fence_init();
+        }
+        pdl_wait_then_release();
+        __syncthreads();
+        if (cluster > 1) cluster_sync_all();  // every block's barriers exist
+    }
+    // The flat elements of the batch of rows that starts at row m, as whole chunks: [begin, end),
+    // end cut at the matrix's last whole chunk.  (With a cluster there is one row, cut to its
+    // slice.)
+    __device__ __forceinline__ void span(const Shape& s, int64_t m, int64_t& begin, int64_t& end) const {
+        const int64_t rows = s.M - m < s.groups ? s.M - m : s.groups;
+        begin = (m * s.K + k0) & ~int64_t(kE - 1);
+        end = ((cluster > 1 ? m * s.K + k0 + ks : (m + rows) * s.K) + kE - 1) & ~int64_t(kE - 1);
+        const int64_t most = (s.M * s.K) & ~int64_t(kE - 1);
+        if (end > most) end = most;
+        if (end < begin) end = begin;
+    }
+    __device__ __forceinline__ void finish(int32_t* err) const {
+        __syncthreads();
+        if (cluster > 1) cluster_sync_all();  // nobody's sums are still on their way here
+        if (threadIdx.x == 0 && *static_cast<volatile int*>(&ctl->abort) && err != nullptr)
+            atomicOr(err, kErrBitTimeout);
+    }
+};
+
+// One lane fills the ring, in the order in which the batches are worked on.
+template <typename TX, typename TD>
+__device__ __forceinline__ void fill_ring(const Place& pl, const Shape& s, const TX* X, const TD* dY) {
+    if (threadIdx.x % 32 != 0) return;
+    long long issued = 0;
+    bool ok = true;
+    for (int64_t m = pl.first; m < s.M; m += pl.step, ++issued) {
+        const int stage = static_cast<int>(issued % s.stages);
+        if (!mbar_wait_bounded(smem_u32(&pl.ctl->empty[stage]), static_cast<uint32_t>(((issued / s.stages) & 1) ^ 1),
+                               &pl.ctl->abort)) {
+            ok = false;
+            break;
+        }
+        const uint32_t bar = smem_u32(&pl.ctl->full[stage]);
+        const uint32_t slot = smem_u32(pl.ring) + static_cast<uint32_t>(stage * (s.slot_x + s.slot_d));
+        int64_t begin, end;
+        pl.span(s, m, begin, end);
+        const uint32_t n = static_cast<uint32_t>(end - begin);
+        mbar_arrive_expect_tx(bar, n * static_cast<uint32_t>(sizeof(TX) + sizeof(TD)));
+        if (n > 0) {
+            bulk_load(slot, X + begin, n * static_cast<uint32_t>(sizeof(TX)), bar);
+            bulk_load(slot + s.slot_x, dY + begin, n * static_cast<uint32_t>(sizeof(TD)), bar);
+        }
+    }
+    if (!ok)  // wait for the copies in flight before the block may leave
+        for (int i = 0; i < s.stages; ++i) {
+            const long long fills = (issued - i + s.stages - 1) / s.stages;
+            if (fills > 0) drain_wait(smem_u32(&pl.ctl->full[i]), static_cast<uint32_t>((fills - 1) & 1));
+        }
+}
+
 struct BwdArgs {
+    Shape s;
+    const float* w;
+    bool layer;
+    float eps, inv_k;
+    void* dx;
+    bool dx_bf16;
+    float* dw;  // [blocks or clusters, K] partial sums (the result itself with one), or NULL
+    float* db;
+    int32_t* err;
+};
+
+// DB: with the bias's gradient (its sums take registers).
+template <typename TX, typename TD, bool EDGE, bool DB, int CH>
+__global__ void __launch_bounds__(CH == 1 ? 800 : 640)
+    norm_backward_kernel(const TX* __restrict__ X, const TD* __restrict__ dY, const __grid_constant__ BwdArgs a) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    const Shape& s = a.s;
+    Place pl(smem, s);
+    const int t = pl.t, tpr = pl.tpr;
+    // this thread's columns: element 0 of chunk c is column k0 + (c tpr + t) 8 - skip
+    const int64_t total = s.M * s.K;
+    const int skip = EDGE ? static_cast<int>(((pl.first + pl.group) * s.K + pl.k0) & (kE - 1)) : 0;
+    Mask mask[CH];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+        const int k = (c * tpr + t) * kE - skip;
+        mask[c] = EDGE ? Mask{k < 0 ? -k : 0, pl.ks - k < kE ? pl.ks - k : kE} : Mask{0, k < pl.ks ? kE : 0};
+    }
+    float dw[CH][kE], db[DB ? CH : 1][kE];
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+        for (int e = 0; e < kE; ++e) {
+            dw[c][e] = 0.0f;
+            if constexpr (DB) db[c][e] = 0.0f;
+        }
+    if (pl.producer) {
+        fill_ring<TX, TD>(pl, s, X, dY);
+    } else {
+        RowSum row_sum{GroupSum{pl.ctl->sums[pl.group], t, tpr, pl.group}, pl.ctl, pl.cluster, pl.rank};
+        float w[CH][kE];
+#pragma unroll
+        for (int c = 0; c < CH; ++c) load_vector<EDGE>(a.w, 1.0f, pl.k0 + (c * tpr + t) * kE - skip, mask[c], w[c]);
+        int stage = 0;
+        uint32_t phase = 0;
+        for (int64_t m0 = pl.first; m0 < s.M; m0 += pl.step) {
+            if (!mbar_wait_bounded(smem_u32(&pl.ctl->full[stage]), phase, &pl.ctl->abort)) break;
+            const int64_t m = m0 + pl.group;
+            const bool live = m < s.M;
+            const int64_t flat0 = m * s.K + pl.k0 - skip;
+            Raw<TX> x[CH];
+            Raw<TD> d[CH];
+            if (live) {
+                int64_t begin, end;
+                pl.span(s, m0, begin, end);
+                const uint8_t* slot = pl.ring + stage * (s.slot_x + s.slot_d);
+                const int at = static_cast<int>(flat0 - begin) + t * kE;
+#pragma unroll
+                for (int c = 0; c < CH; ++c) {
+                    const int i = at + c * tpr * kE;
+                    if (mask[c].any() && (!EDGE || i < static_cast<int>(end - begin))) {
+                        x[c].load(reinterpret_cast<const TX*>(slot) + i);
+                        d[c].load(reinterpret_cast<const TD*>(slot + s.slot_x) + i);
+                    } else {
+                        x[c].clear();
+                        d[c].clear();
+                    }
+                }
+            }
+            __syncwarp();
+            if ((t & 31) == 0) mbar_arrive(smem_u32(&pl.ctl->empty[stage]));
+            if (++stage == s.stages) {
+                stage = 0;
+                phase ^= 1u;
+            }
+            if (!live) continue;  // rows of a batch past the last one: the whole group skips
+            // the values of chunk c, zero where they are not the row's
+            auto values = [&](int c, float(&xv)[kE], float(&dv)[kE]) {
+                if constexpr (EDGE) {
+                    const int64_t flat = flat0 + static_cast<int64_t>(c * tpr + t) * kE;
+                    if (mask[c].any() && flat + kE > total) {
+                        load_flat(X, flat, total, xv);  // the matrix's last chunk
+                        load_flat(dY, flat, total, dv);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < kE; ++e) xv[e] = x[c][e], dv[e] = d[c][e];
+                    }
+                    if (!mask[c].all())
+#pragma unroll
+                        for (int e = 0; e < kE; ++e)
+                            if (!mask[c].has(e)) xv[e] = dv[e] = 0.0f;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < kE; ++e) xv[e] = x[c][e], dv[e] = d[c][e];
+                }
+            };
+            float mu = 0.0f, c2 = 0.0f;
+            if (a.layer) {
+                float sum = 0.0f, sg = 0.0f;
+#pragma unroll
+                for (int c = 0; c < CH; ++c) {
+                    float xv[kE], dv[kE];
+                    values(c, xv, dv);
+#pragma unroll
+                    for (int e = 0; e < kE; ++e) {
+                        sum += xv[e];
+                        sg = fmaf(dv[e], w[c][e], sg);
+                    }
+                }
+                const float2 both = row_sum(sum, sg);
+                mu = both.x * a.inv_k;
+                c2 = both.y * a.inv_k;
+            }
+            float v = 0.0f, gx = 0.0f;
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                if (!mask[c].any()) continue;
+                float xv[kE], dv[kE];
+                values(c, xv, dv);
+#pragma unroll
+                for (int e = 0; e < kE; ++e) {
+                    const float z = !EDGE || mask[c].has(e) ? xv[e] - mu : 0.0f;
+                    v = fmaf(z, z, v);
+                    gx = fmaf(dv[e] * w[c][e], z, gx);
+                }
+            }
+            const float2 both = row_sum(v, gx);
+            const float r = 1.0f / sqrtf(both.x * a.inv_k + a.eps);
+            const float c1 = both.y * a.inv_k * r;
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                if (!mask[c].any()) continue;
+                float xv[kE], dv[kE];
+                values(c, xv, dv);
+#pragma unroll
+                for (int e = 0; e < kE; ++e) {
+                    const float n = (xv[e] - mu) * r;
+                    xv[e] = r * ((dv[e] * w[c][e] - c2) - n * c1);
+                    dw[c][e] = fmaf(dv[e], n, dw[c][e]);
+                    if constexpr (DB) db[c][e] += dv[e];
+                }
+                store_flat(a.dx, a.dx_bf16, flat0 + static_cast<int64_t>(c * tpr + t) * kE, mask[c], xv);
+            }
+        }
+    }
+    if (a.dw != nullptr || DB) {
+        // the groups add their column sums in shared memory, one after the other (the ring is
+        // free: every copy has landed and been read)
+        float* cols = reinterpret_cast<float*>(pl.ring);
+        const int ks = pl.ks;
+        __syncthreads();
+        for (int g = 0; g < s.groups; ++g) {
+            if (!pl.producer && g == pl.group) {
+#pragma unroll
+                for (int c = 0; c < CH; ++c)
+#pragma unroll
+                    for (int e = 0; e < kE; ++e) {
+                        if (!mask[c].has(e)) continue;
+                        const int k = (c * tpr + t) * kE - skip + e;
+                        cols[k] = g > 0 ? cols[k] + dw[c][e] : dw[c][e];
+                        if constexpr (DB) cols[ks + k] = g > 0 ? cols[ks + k] + db[c][e] : db[c][e];
+                    }
+            }
+            __syncthreads();
+        }
+        const int64_t off = static_cast<int64_t>(blockIdx.x / pl.cluster) * s.K + pl.k0;
+        for (int k = threadIdx.x; k < ks; k += blockDim.x) {
+            if (a.dw != nullptr) a.dw[off + k] = cols[k];
+            if constexpr (DB) a.db[off + k] = cols[ks + k];
+        }
+    }
+    pl.finish(a.err);
+}
+
+struct LongBwdArgs {
     const float* w;
     int64_t M, K;
     bool layer;
     float eps, inv_k;
     void* dx;
     bool dx_bf16;
-    float* dw;  // [gridDim.x, K] partial sums (the result itself with one block), or NULL
+    float* dw;  // [strips of rows, K] partial sums (the result itself with one), or NULL
     float* db;
 };
 
-// One row at a time per group; the group's threads keep the column sums of their columns.
-template <typename TX, typename TD, bool VEC, int CH>
-__global__ void __launch_bounds__(CH <= 2 ? 512 : 256)
-    norm_backward_kernel(const TX* __restrict__ X, const TD* __restrict__ dY, const BwdArgs a) {
-    __shared__ float2 sums[kMaxGroups][64];
-    extern __shared__ float cols[];  // [2][tpr * CH * kE] column sums of the block's groups
-    const int t = threadIdx.x, tpr = blockDim.x, group = threadIdx.y, groups = blockDim.y;
-    pdl_wait_then_release();
-    RowSum row_sum{sums[group], t, tpr, group};
-    float dw[CH][kE], db[CH][kE];
-#pragma unroll
-    for (int c = 0; c < CH; ++c)
-#pragma unroll
-        for (int e = 0; e < kE; ++e) dw[c][e] = db[c][e] = 0.0f;
-
-    for (int64_t m = static_cast<int64_t>(blockIdx.x) * groups + group; m < a.M;
-         m += static_cast<int64_t>(gridDim.x) * groups) {
-        const TX* row = X + m * a.K;
-        const TD* drow = dY + m * a.K;
-        float x[CH][kE], d[CH][kE];
-#pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            load_chunk<VEC>(row, c, t, tpr, a.K, x[c]);
-            load_chunk<VEC>(drow, c, t, tpr, a.K, d[c]);
-        }
-        float mu = 0.0f, c2 = 0.0f;
-        if (a.layer) {
-            float s = 0.0f, sg = 0.0f;
-#pragma unroll
-            for (int c = 0; c < CH; ++c) {
-                float w[kE];
-                if (a.w != nullptr) load_chunk<VEC>(a.w, c, t, tpr, a.K, w);
-#pragma unroll
-                for (int e = 0; e < kE; ++e) {
-                    s += x[c][e];
-                    sg = a.w != nullptr ? fmaf(d[c][e], w[e], sg) : sg + d[c][e];
-                }
-            }
-            const float2 both = row_sum(s, sg);
-            mu = both.x * a.inv_k;
-            c2 = both.y * a.inv_k;
-        }
-        float v = 0.0f, gx = 0.0f;
-#pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            float w[kE];
-            if (a.w != nullptr) load_chunk<VEC>(a.w, c, t, tpr, a.K, w);
-#pragma unroll
-            for (int e = 0; e < kE; ++e) {
-                if (elem<VEC>(c, e, t, tpr) < a.K) {
-                    x[c][e] -= mu;
-                    v = fmaf(x[c][e], x[c][e], v);
-                    const float g = a.w != nullptr ? d[c][e] * w[e] : d[c][e];
-                    gx = fmaf(g, x[c][e], gx);
-                }
-            }
-        }
-        const float2 both = row_sum(v, gx);
-        const float r = 1.0f / sqrtf(both.x * a.inv_k + a.eps);
-        const float c1 = both.y * a.inv_k * r;
-#pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            float w[kE], o[kE];
-            if (a.w != nullptr) load_chunk<VEC>(a.w, c, t, tpr, a.K, w);
-#pragma unroll
-            for (int e = 0; e < kE; ++e) {
-                const float n = x[c][e] * r;
-                const float g = a.w != nullptr ? d[c][e] * w[e] : d[c][e];
-                o[e] = r * ((g - c2) - n * c1);
-                dw[c][e] = fmaf(d[c][e], n, dw[c][e]);
-                db[c][e] += d[c][e];
-            }
-            store_chunk<VEC>(a.dx, a.dx_bf16, m * a.K, c, t, tpr, a.K, o);
-        }
-    }
-    if (a.dw == nullptr && a.db == nullptr) return;
-    // the groups add their column sums in shared memory, one after the other
-    const int width = tpr * CH * kE;
-    for (int g = 0; g < groups; ++g) {
-        if (g == group) {
-#pragma unroll
-            for (int c = 0; c < CH; ++c)
-#pragma unroll
-                for (int e = 0; e < kE; ++e) {
-                    const int k = (c * kE + e) * tpr + t;
-                    if (g == 0) {
-                        cols[k] = dw[c][e];
-                        cols[width + k] = db[c][e];
-                    } else {
-                        cols[k] = dw[c][e] += cols[k];
-                        cols[width + k] = db[c][e] += cols[width + k];
-                    }
-                }
-        }
-        if (g + 1 < groups) __syncthreads();
-    }
-    if (group + 1 != groups) return;
-    const int64_t off = static_cast<int64_t>(blockIdx.x) * a.K;
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-        // rows of a partial-sum matrix start anywhere: element stores unless K % 8 == 0
-        if (a.dw != nullptr) store_chunk<VEC>(a.dw, false, off, c, t, tpr, a.K, dw[c]);
-        if (a.db != nullptr) store_chunk<VEC>(a.db, false, off, c, t, tpr, a.K, db[c]);
-    }
-}
-
-// Rows too long for the registers: dx row by row as in norm_forward_long_kernel, keeping
+// Rows longer than a cluster's slices: dx row by row as in norm_forward_long_kernel, keeping
 // (mu, r) of every row for the column kernel below.
 template <typename TX, typename TD>
 __global__ void __launch_bounds__(kMaxThreads)
-    norm_backward_long_kernel(const TX* __restrict__ X, const TD* __restrict__ dY, const BwdArgs a,
+    norm_backward_long_kernel(const TX* __restrict__ X, const TD* __restrict__ dY, const LongBwdArgs a,
                               float2* __restrict__ stats) {
     __shared__ float2 sums[64];
     const int t = threadIdx.x, tpr = blockDim.x;
     pdl_wait_then_release();
-    RowSum row_sum{sums, t, tpr, 0};
+    BlockSum row_sum{sums, t, tpr};
     const int64_t m = blockIdx.x;
     const TX* row = X + m * a.K;
     const TD* drow = dY + m * a.K;
@@ -414,7 +743,7 @@ __global__ void __launch_bounds__(kMaxThreads)
 // Column sums of a strip of rows from x, dy and the rows' (mu, r): a thread owns a column.
 template <typename TX, typename TD>
 __global__ void __launch_bounds__(256)
-    norm_columns_long_kernel(const TX* __restrict__ X, const TD* __restrict__ dY, const BwdArgs a,
+    norm_columns_long_kernel(const TX* __restrict__ X, const TD* __restrict__ dY, const LongBwdArgs a,
                              const float2* __restrict__ stats, int64_t rows_per_block) {
     pdl_wait_then_release();
     const int64_t m0 = blockIdx.x * rows_per_block;
@@ -454,94 +783,155 @@ __global__ void __launch_bounds__(1024)
     if (threadIdx.x == 0 && ko < K) out[ko] = v;
 }
 
-// Threads of a row and row groups of a block for rows of K elements in CH chunks a thread.
-struct Shape {
-    int tpr, groups;
-};
-Shape shape_of(int64_t K, int ch) {
-    const int64_t chunks = (K + kE - 1) / kE;
-    const int tpr = static_cast<int>((chunks + ch - 1) / ch + 31) / 32 * 32;
-    int groups = 256 / tpr;
-    return Shape{tpr, groups < 1 ? 1 : groups > kMaxGroups ? kMaxGroups : groups};
-}
+// --------------------------------------------------------------------- launches --
 
-constexpr int64_t kFwdMaxK = int64_t(kMaxThreads) * 4 * kE;
-constexpr int64_t kBwdMaxK = int64_t(256) * 4 * kE;
+// Chunks that a row of K elements can touch.
+int64_t chunks_of(int64_t K) { return K % kE == 0 ? K / kE : (K + kE - 2) / kE + 1; }
 
-// Chunks a thread: one for rows that then still fill a warp group, up to four.
-int chunks_of(int64_t K) {
-    const int64_t chunks = (K + kE - 1) / kE;
-    return chunks <= 128 ? 1 : chunks <= 256 ? 2 : 4;
-}
+// Forward: up to 8192 columns in blocks of up to 256 threads, many of which share an SM; longer
+// rows in one block of up to 1024 threads with four chunks each.
+constexpr int64_t kFwdMaxChunks = int64_t(kMaxThreads) * 4;
 
-template <typename TX, bool VEC>
+template <typename TX, bool EDGE>
 cudaError_t forward_t(const TX* X, const FwdArgs& a, cudaStream_t stream) {
-    const int ch = chunks_of(a.K);
-    const Shape s = shape_of(a.K, ch);
-    const dim3 grid(static_cast<unsigned>((a.M + s.groups - 1) / s.groups)), block(s.tpr, s.groups);
-    switch (ch) {
-        case 1: return launch_pdl(norm_forward_kernel<TX, VEC, 1>, grid, block, 0, stream, dim3(kNoCluster), X, a);
-        case 2: return launch_pdl(norm_forward_kernel<TX, VEC, 2>, grid, block, 0, stream, dim3(kNoCluster), X, a);
-        default: return launch_pdl(norm_forward_kernel<TX, VEC, 4>, grid, block, 0, stream, dim3(kNoCluster), X, a);
-    }
+    const int64_t chunks = chunks_of(a.K);
+    const int ch = chunks <= 128 ? 1 : chunks <= 256 ? 2 : 4;
+    const int tpr = static_cast<int>(((chunks + ch - 1) / ch + 31) / 32 * 32);
+    // several rows share a block of 256 threads, as long as the blocks still cover the SMs
+    int groups = 256 / tpr;
+    if (groups > (a.M + kParts - 1) / kParts) groups = static_cast<int>((a.M + kParts - 1) / kParts);
+    if (groups < 1) groups = 1;
+    const dim3 grid(static_cast<unsigned>((a.M + groups - 1) / groups)), block(tpr, groups);
+    auto run = [&](auto kernel) { return launch_pdl(kernel, grid, block, 0, stream, dim3(kNoCluster), X, a); };
+    if (ch == 1) return run(norm_forward_kernel<TX, EDGE, 1, 256, 6>);
+    if (ch == 2) return run(norm_forward_kernel<TX, EDGE, 2, 256, 5>);
+    if (tpr <= 256) return run(norm_forward_kernel<TX, EDGE, 4, 256, sizeof(TX) == 2 && !EDGE ? 5 : 4>);
+    return run(norm_forward_kernel<TX, EDGE, 4, kMaxThreads, 1>);
 }
 
 template <typename TX>
 cudaError_t forward_x(const TX* X, const FwdArgs& a, cudaStream_t stream) {
-    if (a.K > kFwdMaxK)
+    if (chunks_of(a.K) > kFwdMaxChunks)
         return launch_pdl(norm_forward_long_kernel<TX>, dim3(static_cast<unsigned>(a.M)), dim3(kMaxThreads), 0, stream,
                           dim3(kNoCluster), X, a);
-    return a.K % kE == 0 ? forward_t<TX, true>(X, a, stream) : forward_t<TX, false>(X, a, stream);
+    return a.K % kE == 0 ? forward_t<TX, false>(X, a, stream) : forward_t<TX, true>(X, a, stream);
 }
 
-// Blocks of the backward: each leaves one row of partial column sums.
-int backward_blocks(int64_t M, int64_t K) {
-    const int64_t per = K <= kBwdMaxK ? shape_of(K, chunks_of(K)).groups : 16;
-    const int64_t want = (M + per - 1) / per;
-    const int64_t most = 2 * 148;
-    return static_cast<int>(want < most ? want : most);
+// Backward: how rows of K columns are laid over blocks.  Up to 4096 columns a thread owns one
+// chunk, up to kSlice two; longer rows go to the smallest cluster whose slices fit (a power of
+// two up to eight).  Several rows share a block as long as the rows still spread over all SMs.
+struct Plan {
+    int cluster, chunks;  // blocks of a row, chunks of a thread
+    Shape s;
+    int parts;            // blocks or clusters
+};
+
+bool is_long(int64_t K) { return K > int64_t(kSlice) * kMaxCluster; }
+
+Plan plan_of(int64_t M, int64_t K, int ex, int ed) {
+    Plan p{};
+    p.cluster = 1;
+    while ((K + p.cluster - 1) / p.cluster > kSlice) p.cluster *= 2;
+    const int64_t slice = ((K + p.cluster - 1) / p.cluster + kE - 1) / kE * kE;
+    const int64_t chunks = chunks_of(p.cluster > 1 ? slice - (K % kE != 0) : K);  // unaligned: one more
+    p.chunks = chunks <= 513 ? 1 : 2;
+    Shape& s = p.s;
+    s.M = M;
+    s.K = K;
+    s.slice = static_cast<int>(p.cluster > 1 ? slice : K);
+    s.tpr = static_cast<int>(((chunks + p.chunks - 1) / p.chunks + 31) / 32 * 32);
+    const int64_t spread = (M + kParts - 1) / kParts;  // rows of a block when all SMs have some
+    const int fit = p.cluster > 1 ? 1 : (p.chunks == 1 ? 768 : 608) / s.tpr;
+    s.groups = fit < kMaxGroups ? fit : kMaxGroups;
+    if (s.groups > spread) s.groups = static_cast<int>(spread);
+    const int64_t batches = (M + s.groups - 1) / s.groups;
+    const int most = kParts / p.cluster;
+    p.parts = static_cast<int>(batches < most ? batches : most);
+    if (K % kE != 0) {
+        // rows in step a multiple of eight (see Shape)
+        int unit = kE;
+        while (unit > 1 && (unit / 2) * s.groups % kE == 0) unit /= 2;
+        p.parts = p.parts < unit ? unit : p.parts / unit * unit;
+    }
+    // a slot: the rows' elements and up to seven on either side
+    const int64_t cols = ((p.cluster > 1 ? slice : K * s.groups) + 2 * kE) / kE * kE + kE;
+    s.slot_x = static_cast<int>(cols * ex);
+    s.slot_d = static_cast<int>(cols * ed);
+    const int n = kRingBytes / (s.slot_x + s.slot_d);
+    s.stages = n < kMaxStages ? n : kMaxStages;
+    return p;
 }
 
-template <typename TX, typename TD, bool VEC, int CH>
-cudaError_t backward_c(const TX* X, const TD* dY, const BwdArgs& a, cudaStream_t stream) {
-    const Shape s = shape_of(a.K, CH);
-    const size_t smem = static_cast<size_t>(2) * s.tpr * CH * kE * sizeof(float);
+size_t smem_of(const Plan& p) {
+    size_t ring = static_cast<size_t>(p.s.stages) * (p.s.slot_x + p.s.slot_d);
+    const size_t cols = static_cast<size_t>(2) * p.s.slice * sizeof(float);  // column sums
+    if (ring < cols) ring = cols;
+    return ((sizeof(Control) + 127) & ~size_t(127)) + ring;
+}
+
+constexpr int kSmemMost = 227 * 1024;
+static_assert(((sizeof(Control) + 127) & ~size_t(127)) + kRingBytes <= kSmemMost, "shared memory");
+
+int backward_parts(int64_t M, int64_t K) {
+    if (!is_long(K)) return plan_of(M, K, 4, 4).parts;  // does not depend on the types
+    const int64_t strips = (M + 15) / 16;
+    return static_cast<int>(strips < kParts ? strips : kParts);
+}
+
+template <typename TX, typename TD, bool EDGE, bool DB, int CH>
+cudaError_t backward_c(const TX* X, const TD* dY, const Plan& p, const BwdArgs& a, cudaStream_t stream) {
     static PerContextOnce attr;
     cudaError_t e = attr.run([] {
-        return cudaFuncSetAttribute(norm_backward_kernel<TX, TD, VEC, CH>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    static_cast<int>(2 * 256 * 4 * kE * sizeof(float)));
+        return cudaFuncSetAttribute(norm_backward_kernel<TX, TD, EDGE, DB, CH>,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost);
     });
     if (e != cudaSuccess) return e;
-    return launch_pdl(norm_backward_kernel<TX, TD, VEC, CH>, dim3(backward_blocks(a.M, a.K)), dim3(s.tpr, s.groups),
-                      smem, stream, dim3(kNoCluster), X, dY, a);
+    return launch_pdl(norm_backward_kernel<TX, TD, EDGE, DB, CH>, dim3(static_cast<unsigned>(p.parts * p.cluster)),
+                      dim3(p.s.tpr * p.s.groups + 32), smem_of(p), stream,
+                      p.cluster > 1 ? dim3(p.cluster, 1, 1) : dim3(kNoCluster), X, dY, a);
 }
 
+template <typename TX, typename TD, bool EDGE>
+cudaError_t backward_e(const TX* X, const TD* dY, const Plan& p, const BwdArgs& a, cudaStream_t stream) {
+    if (a.db != nullptr)
+        return p.chunks == 1 ? backward_c<TX, TD, EDGE, true, 1>(X, dY, p, a, stream)
+                             : backward_c<TX, TD, EDGE, true, 2>(X, dY, p, a, stream);
+    return p.chunks == 1 ? backward_c<TX, TD, EDGE, false, 1>(X, dY, p, a, stream)
+                         : backward_c<TX, TD, EDGE, false, 2>(X, dY, p, a, stream);
+}
+
+struct BwdCall {
+    const float* w;
+    int64_t M, K;
+    bool layer;
+    float eps;
+    void* dx;
+    bool dx_bf16;
+    float* dw;  // where the kernels leave their sums: partial ones with several parts
+    float* db;
+    float2* stats;
+    int parts;
+    int32_t* err;
+};
+
 template <typename TX, typename TD>
-cudaError_t backward_t(const TX* X, const TD* dY, const BwdArgs& a, float2* stats, cudaStream_t stream) {
-    if (a.K > kBwdMaxK) {
-        cudaError_t e = launch_pdl(norm_backward_long_kernel<TX, TD>, dim3(static_cast<unsigned>(a.M)),
-                                   dim3(kMaxThreads), 0, stream, dim3(kNoCluster), X, dY, a, stats);
-        if (e != cudaSuccess || (a.dw == nullptr && a.db == nullptr)) return e;
-        const int parts = backward_blocks(a.M, a.K);
-        const int64_t rows = (a.M + parts - 1) / parts;
-        const int64_t strips = (a.K + 255) / 256;
+cudaError_t backward_t(const TX* X, const TD* dY, const BwdCall& c, cudaStream_t stream) {
+    const float inv_k = 1.0f / static_cast<float>(c.K);
+    if (is_long(c.K)) {
+        const LongBwdArgs a{c.w, c.M, c.K, c.layer, c.eps, inv_k, c.dx, c.dx_bf16, c.dw, c.db};
+        cudaError_t e = launch_pdl(norm_backward_long_kernel<TX, TD>, dim3(static_cast<unsigned>(c.M)),
+                                   dim3(kMaxThreads), 0, stream, dim3(kNoCluster), X, dY, a, c.stats);
+        if (e != cudaSuccess || (c.dw == nullptr && c.db == nullptr)) return e;
+        const int64_t rows = (c.M + c.parts - 1) / c.parts;
+        const int64_t strips = (c.K + 255) / 256;
         return launch_pdl(norm_columns_long_kernel<TX, TD>,
-                          dim3(parts, static_cast<unsigned>(strips < 65535 ? strips : 65535)), dim3(256), 0, stream,
-                          dim3(kNoCluster), X, dY, a, static_cast<const float2*>(stats), rows);
+                          dim3(c.parts, static_cast<unsigned>(strips < 65535 ? strips : 65535)), dim3(256), 0, stream,
+                          dim3(kNoCluster), X, dY, a, static_cast<const float2*>(c.stats), rows);
     }
-    const int ch = chunks_of(a.K);
-    if (a.K % kE == 0) {
-        switch (ch) {
-            case 1: return backward_c<TX, TD, true, 1>(X, dY, a, stream);
-            case 2: return backward_c<TX, TD, true, 2>(X, dY, a, stream);
-            default: return backward_c<TX, TD, true, 4>(X, dY, a, stream);
-        }
-    }
-    switch (ch) {
-        case 1: return backward_c<TX, TD, false, 1>(X, dY, a, stream);
-        case 2: return backward_c<TX, TD, false, 2>(X, dY, a, stream);
-        default: return backward_c<TX, TD, false, 4>(X, dY, a, stream);
-    }
+    const Plan p = plan_of(c.M, c.K, sizeof(TX), sizeof(TD));
+    const BwdArgs a{p.s, c.w, c.layer, c.eps, inv_k, c.dx, c.dx_bf16, c.dw, c.db, c.err};
+    return c.K % kE == 0 ? backward_e<TX, TD, false>(X, dY, p, a, stream)
+                         : backward_e<TX, TD, true>(X, dY, p, a, stream);
 }
 
 int64_t align16(int64_t n) { return (n + 15) / 16 * 16; }
@@ -555,42 +945,41 @@ cudaError_t launch_norm_forward(const void* X, bool x_bf16, const float* w, cons
                   : forward_x(static_cast<const float*>(X), a, stream);
 }
 
-// Partial column sums of dw and db, and the rows' statistics for rows that do not fit the
-// registers.
+// Partial column sums of dw and db, and the statistics of rows longer than a cluster's slices.
 size_t norm_backward_workspace(int64_t M, int64_t K) {
-    const int64_t parts = backward_blocks(M, K);
+    const int64_t parts = backward_parts(M, K);
     int64_t bytes = parts > 1 ? 2 * align16(parts * K * 4) : 0;
-    if (K > kBwdMaxK) bytes += align16(M * 8);
+    if (is_long(K)) bytes += align16(M * 8);
     return static_cast<size_t>(bytes);
 }
 
 cudaError_t launch_norm_backward(const void* dY, bool dy_bf16, const void* X, bool x_bf16, const float* w, int64_t M,
                                  int64_t K, int kind, float eps, void* dX, bool dx_bf16, float* dw, float* db,
-                                 void* ws, cudaStream_t stream) {
-    const int parts = backward_blocks(M, K);
+                                 void* ws, int32_t* err, cudaStream_t stream) {
+    const int parts = backward_parts(M, K);
     const int64_t part_bytes = align16(static_cast<int64_t>(parts) * K * 4);
     uint8_t* p = static_cast<uint8_t*>(ws);
-    BwdArgs a{w, M, K, kind == 1, eps, 1.0f / static_cast<float>(K), dX, dx_bf16, dw, db};
+    BwdCall c{w, M, K, kind == 1, eps, dX, dx_bf16, dw, db, nullptr, parts, err};
     if (parts > 1) {
-        if (dw != nullptr) a.dw = reinterpret_cast<float*>(p);
-        if (db != nullptr) a.db = reinterpret_cast<float*>(p + part_bytes);
+        if (dw != nullptr) c.dw = reinterpret_cast<float*>(p);
+        if (db != nullptr) c.db = reinterpret_cast<float*>(p + part_bytes);
         p += 2 * part_bytes;
     }
-    float2* stats = K > kBwdMaxK ? reinterpret_cast<float2*>(p) : nullptr;
+    if (is_long(K)) c.stats = reinterpret_cast<float2*>(p);
     cudaError_t e;
     if (x_bf16) {
         const auto* x = static_cast<const __nv_bfloat16*>(X);
-        e = dy_bf16 ? backward_t(x, static_cast<const __nv_bfloat16*>(dY), a, stats, stream)
-                    : backward_t(x, static_cast<const float*>(dY), a, stats, stream);
+        e = dy_bf16 ? backward_t(x, static_cast<const __nv_bfloat16*>(dY), c, stream)
+                    : backward_t(x, static_cast<const float*>(dY), c, stream);
     } else {
         const auto* x = static_cast<const float*>(X);
-        e = dy_bf16 ? backward_t(x, static_cast<const __nv_bfloat16*>(dY), a, stats, stream)
-                    : backward_t(x, static_cast<const float*>(dY), a, stats, stream);
+        e = dy_bf16 ? backward_t(x, static_cast<const __nv_bfloat16*>(dY), c, stream)
+                    : backward_t(x, static_cast<const float*>(dY), c, stream);
     }
     if (e != cudaSuccess || parts == 1 || (dw == nullptr && db == nullptr)) return e;
     const dim3 grid(static_cast<unsigned>((K + 31) / 32), dw != nullptr && db != nullptr ? 2 : 1);
     return launch_pdl(norm_reduce_kernel, grid, dim3(32, 32), 0, stream, dim3(kNoCluster),
-                      static_cast<const float*>(a.dw), static_cast<const float*>(a.db), parts, K, dw, db);
+                      static_cast<const float*>(c.dw), static_cast<const float*>(c.db), parts, K, dw, db);
 }
 
 }  // namespace bl

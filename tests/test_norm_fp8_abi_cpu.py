@@ -40,8 +40,8 @@ def test_norm_backward_refusals(L):
     f = L.bitlinear_norm_backward
     need = L.bitlinear_norm_backward_workspace_size(64, 512)
     assert need > 0
-    #       dY    type X     type  w     M   K    kind   eps   dX    type dw    db    ws    bytes stream
-    good = [FAKE, F32, FAKE, BF16, FAKE, 64, 512, LAYER, 1e-5, FAKE, F32, FAKE, FAKE, FAKE, need, None]
+    #       dY    type X     type  w     M   K    kind   eps   dX    type dw    db    ws    bytes err   stream
+    good = [FAKE, F32, FAKE, BF16, FAKE, 64, 512, LAYER, 1e-5, FAKE, F32, FAKE, FAKE, FAKE, need, None, None]
     for i, v, want in [(0, None, INVALID), (1, I32, INVALID), (2, None, INVALID), (3, I32, INVALID), (5, 0, INVALID),
                        (6, 0, INVALID), (5, BIG, SHAPE), (6, BIG, SHAPE), (7, 5, INVALID), (8, -1.0, INVALID),
                        (9, None, INVALID), (10, I32, INVALID), (0, ODD, MISALIGNED), (2, ODD, MISALIGNED),

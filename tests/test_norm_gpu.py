@@ -101,7 +101,8 @@ def close(got, want, tol, what):
 
 
 SHAPES = [(1, 1), (3, 5), (1, 8), (2, 31), (7, 256), (33, 1000), (5, 1537), (64, 1536), (16, 3200), (301, 4096),
-          (9, 8192), (17, 8640), (3, 9999), (5, 16384), (2, 28672), (3, 32768), (2, 32769), (2, 40000)]
+          (9, 8192), (17, 8640), (3, 9999), (5, 16384), (2, 28672), (3, 32768), (2, 32769), (2, 40000), (3, 77696), (9, 9705), (10, 9712), (9, 9713), (30, 4097), (25, 4104),
+          (2, 77697), (3, 80003), (2, 77689)]
 
 
 @pytest.mark.parametrize("M,K", SHAPES)
@@ -172,7 +173,7 @@ def test_backward_against_differences(kind):
         assert (got.double() - want).abs().max() <= (64 * U + 1e-8) * want.abs().max()
 
 
-@pytest.mark.parametrize("K", [256, 1537, 8640, 40000])
+@pytest.mark.parametrize("K", [256, 1537, 8640, 40000, 80000])
 def test_non_finite_values_spread_as_the_formulas_say(K):
     x, w, _, dy = inputs(6, K, seed=2, xt=F32)
     x[1, K // 2], x[3, 0] = float("nan"), float("inf")
