@@ -30,7 +30,7 @@
 // their row sums through distributed shared memory.
 //
 // The column sums of the backward stay in the registers of the threads that own the columns
-// while a block walks over its rows; they are added over the rows of a block in shared memory
+// while a block walks over its rows; they are added over the groups of a block in shared memory
 // and over the blocks by a second kernel, always in the same order, so the results do not
 // change from run to run.
 #include <cuda_bf16.h>
@@ -198,44 +198,49 @@ struct FwdArgs {
     bool out_bf16;
 };
 
-// block: x = threads of a row, y = rows.  EDGE: rows are not whole chunks.
-template <typename TX, bool EDGE, int CH, int THREADS, int BLOCKS>
+// block: x = threads of a row, y = groups of them.  A group takes R neighbouring rows together:
+// their sums share a latency and they share the loads of weight and bias.  EDGE: rows are not
+// whole chunks.
+template <typename TX, bool EDGE, int CH, int R, int THREADS, int BLOCKS>
 __global__ void __launch_bounds__(THREADS, BLOCKS) norm_forward_kernel(const TX* __restrict__ X, const FwdArgs a) {
     __shared__ float2 sums[8][64];
     const int t = threadIdx.x, tpr = blockDim.x, group = threadIdx.y;
     pdl_wait_then_release();
     GroupSum row_sum{sums[group], t, tpr, group};
-    const int64_t m = static_cast<int64_t>(blockIdx.x) * blockDim.y + group;
-    if (m >= a.M) return;  // a whole group leaves together
-    const int64_t first = m * a.K;
-    const int skip = EDGE ? static_cast<int>(first & (kE - 1)) : 0;  // of the first chunk
-    const int64_t flat0 = first - skip;
-    auto mask = [&](int c) {
-        const int64_t k = static_cast<int64_t>(c * tpr + t) * kE - skip;  // column of the chunk's element 0
+    const int64_t m0 = (static_cast<int64_t>(blockIdx.x) * blockDim.y + group) * R;
+    if (m0 >= a.M) return;  // a whole group leaves together
+    const int64_t total = a.M * a.K;
+    // row r: element 0 of its chunk c is flat element flat(r, c), column col(r, c) of the row
+    auto skip = [&](int r) { return EDGE ? static_cast<int>((m0 + r) * a.K & (kE - 1)) : 0; };
+    auto col = [&](int r, int c) { return static_cast<int64_t>(c * tpr + t) * kE - skip(r); };
+    auto flat = [&](int r, int c) { return (m0 + r) * a.K + col(r, c); };
+    auto mask = [&](int r, int c) {
+        const int64_t k = col(r, c);
+        if (R > 1 && m0 + r >= a.M) return Mask{0, 0};
         if constexpr (EDGE)
             return Mask{k < 0 ? static_cast<int>(-k) : 0, a.K - k < kE ? static_cast<int>(a.K - k) : kE};
         else
             return Mask{0, k < a.K ? kE : 0};
     };
-    Raw<TX> x[CH];
+    Raw<TX> x[R][CH];
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-        const int64_t flat = flat0 + static_cast<int64_t>(c * tpr + t) * kE;
-        if (mask(c).any() && (!EDGE || flat + kE <= a.M * a.K))
-            x[c].load_global(X + flat);
-        else
-            x[c].clear();
-    }
-    // the values of chunk c, zero where they are not the row's
-    auto values = [&](int c, float(&v)[kE]) {
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            if (mask(r, c).any() && (!EDGE || flat(r, c) + kE <= total))
+                x[r][c].load_global(X + flat(r, c));
+            else
+                x[r][c].clear();
+        }
+    // the values of chunk c of row r, zero where they are not the row's
+    auto values = [&](int r, int c, float(&v)[kE]) {
         if constexpr (EDGE) {
-            const int64_t flat = flat0 + static_cast<int64_t>(c * tpr + t) * kE;
-            const Mask k = mask(c);
-            if (k.any() && flat + kE > a.M * a.K) {
-                load_flat(X, flat, a.M * a.K, v);  // the matrix's last chunk
+            const Mask k = mask(r, c);
+            if (k.any() && flat(r, c) + kE > total) {
+                load_flat(X, flat(r, c), total, v);  // the matrix's last chunk
             } else {
 #pragma unroll
-                for (int e = 0; e < kE; ++e) v[e] = x[c][e];
+                for (int e = 0; e < kE; ++e) v[e] = x[r][c][e];
             }
             if (!k.all())
 #pragma unroll
@@ -243,47 +248,67 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_forward_kernel(const TX*
                     if (!k.has(e)) v[e] = 0.0f;
         } else {
 #pragma unroll
-            for (int e = 0; e < kE; ++e) v[e] = x[c][e];
+            for (int e = 0; e < kE; ++e) v[e] = x[r][c][e];
         }
     };
-    float mu = 0.0f;
+    // both of the sums that GroupSum takes are of rows: row 0 and row R - 1
+    float mu[R], rstd[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) mu[r] = 0.0f;
     if (a.layer) {
-        float s = 0.0f;
+        float s[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            s[r] = 0.0f;
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                float v[kE];
+                values(r, c, v);
+#pragma unroll
+                for (int e = 0; e < kE; ++e) s[r] += v[e];
+            }
+        }
+        const float2 both = row_sum(s[0], R > 1 ? s[R - 1] : 0.0f);
+        mu[0] = both.x * a.inv_k;
+        if constexpr (R > 1) mu[1] = both.y * a.inv_k;
+    }
+    float q[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        q[r] = 0.0f;
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
+            const Mask k = mask(r, c);
+            if (!k.any()) continue;
             float v[kE];
-            values(c, v);
+            values(r, c, v);
 #pragma unroll
-            for (int e = 0; e < kE; ++e) s += v[e];
-        }
-        mu = row_sum(s, 0.0f).x * a.inv_k;
-    }
-    float q = 0.0f;
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-        const Mask k = mask(c);
-        if (!k.any()) continue;
-        float v[kE];
-        values(c, v);
-#pragma unroll
-        for (int e = 0; e < kE; ++e) {
-            const float z = !EDGE || k.has(e) ? v[e] - mu : 0.0f;
-            q = fmaf(z, z, q);
+            for (int e = 0; e < kE; ++e) {
+                const float z = !EDGE || k.has(e) ? v[e] - mu[r] : 0.0f;
+                q[r] = fmaf(z, z, q[r]);
+            }
         }
     }
-    const float r = 1.0f / sqrtf(row_sum(q, 0.0f).x * a.inv_k + a.eps);
+    const float2 both = row_sum(q[0], R > 1 ? q[R - 1] : 0.0f);
+    rstd[0] = 1.0f / sqrtf(both.x * a.inv_k + a.eps);
+    if constexpr (R > 1) rstd[1] = 1.0f / sqrtf(both.y * a.inv_k + a.eps);
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-        const Mask k = mask(c);
-        if (!k.any()) continue;
-        const int64_t col = static_cast<int64_t>(c * tpr + t) * kE - skip;
-        float v[kE], w[kE], b[kE];
-        values(c, v);
-        load_vector<EDGE>(a.w, 1.0f, col, k, w);
-        load_vector<EDGE>(a.b, 0.0f, col, k, b);
+        float w[kE], b[kE];
 #pragma unroll
-        for (int e = 0; e < kE; ++e) v[e] = (v[e] - mu) * r * w[e] + b[e];
-        store_flat(a.out, a.out_bf16, flat0 + static_cast<int64_t>(c * tpr + t) * kE, k, v);
+        for (int r = 0; r < R; ++r) {
+            const Mask k = mask(r, c);
+            if (EDGE || r == 0) {  // whole chunks have the same columns in every row
+                load_vector<EDGE>(a.w, 1.0f, col(r, c), k, w);
+                load_vector<EDGE>(a.b, 0.0f, col(r, c), k, b);
+            }
+            if (!k.any()) continue;
+            float v[kE];
+            values(r, c, v);
+#pragma unroll
+            for (int e = 0; e < kE; ++e) v[e] = (v[e] - mu[r]) * rstd[r] * w[e] + b[e];
+            store_flat(a.out, a.out_bf16, flat(r, c), k, v);
+        }
     }
 }
 
@@ -653,29 +678,43 @@ __global__ void __launch_bounds__(CH == 1 ? 800 : 640)
         }
     }
     if (a.dw != nullptr || DB) {
-        // the groups add their column sums in shared memory, one after the other (the ring is
-        // free: every copy has landed and been read)
+        // every group leaves its column sums in shared memory (the ring is free: every copy has
+        // landed and been read), and they are added in the groups' order
         float* cols = reinterpret_cast<float*>(pl.ring);
-        const int ks = pl.ks;
+        const int ks = pl.ks, all = s.groups * ks;
         __syncthreads();
-        for (int g = 0; g < s.groups; ++g) {
-            if (!pl.producer && g == pl.group) {
+        if (!pl.producer) {
 #pragma unroll
-                for (int c = 0; c < CH; ++c)
+            for (int c = 0; c < CH; ++c) {
+                const int k = (c * tpr + t) * kE - skip;
+                float* p = cols + pl.group * ks + k;
+                if (!EDGE && mask[c].any()) {
+                    *reinterpret_cast<float4*>(p) = make_float4(dw[c][0], dw[c][1], dw[c][2], dw[c][3]);
+                    *reinterpret_cast<float4*>(p + 4) = make_float4(dw[c][4], dw[c][5], dw[c][6], dw[c][7]);
+                    if constexpr (DB) {
+                        *reinterpret_cast<float4*>(p + all) = make_float4(db[c][0], db[c][1], db[c][2], db[c][3]);
+                        *reinterpret_cast<float4*>(p + all + 4) = make_float4(db[c][4], db[c][5], db[c][6], db[c][7]);
+                    }
+                } else {
 #pragma unroll
                     for (int e = 0; e < kE; ++e) {
                         if (!mask[c].has(e)) continue;
-                        const int k = (c * tpr + t) * kE - skip + e;
-                        cols[k] = g > 0 ? cols[k] + dw[c][e] : dw[c][e];
-                        if constexpr (DB) cols[ks + k] = g > 0 ? cols[ks + k] + db[c][e] : db[c][e];
+                        p[e] = dw[c][e];
+                        if constexpr (DB) p[all + e] = db[c][e];
                     }
+                }
             }
-            __syncthreads();
         }
+        __syncthreads();
         const int64_t off = static_cast<int64_t>(blockIdx.x / pl.cluster) * s.K + pl.k0;
         for (int k = threadIdx.x; k < ks; k += blockDim.x) {
-            if (a.dw != nullptr) a.dw[off + k] = cols[k];
-            if constexpr (DB) a.db[off + k] = cols[ks + k];
+            float sw = 0.0f, sb = 0.0f;
+            for (int g = 0; g < s.groups; ++g) {
+                sw += cols[g * ks + k];
+                if constexpr (DB) sb += cols[all + g * ks + k];
+            }
+            if (a.dw != nullptr) a.dw[off + k] = sw;
+            if constexpr (DB) a.db[off + k] = sb;
         }
     }
     pl.finish(a.err);
@@ -797,16 +836,27 @@ cudaError_t forward_t(const TX* X, const FwdArgs& a, cudaStream_t stream) {
     const int64_t chunks = chunks_of(a.K);
     const int ch = chunks <= 128 ? 1 : chunks <= 256 ? 2 : 4;
     const int tpr = static_cast<int>(((chunks + ch - 1) / ch + 31) / 32 * 32);
-    // several rows share a block of 256 threads, as long as the blocks still cover the SMs
+    // several rows share a block of 256 threads, and a group takes two rows, as long as the
+    // blocks still cover the SMs
+    const int64_t spread = (a.M + kParts - 1) / kParts;
     int groups = 256 / tpr;
-    if (groups > (a.M + kParts - 1) / kParts) groups = static_cast<int>((a.M + kParts - 1) / kParts);
+    if (groups > spread) groups = static_cast<int>(spread);
     if (groups < 1) groups = 1;
-    const dim3 grid(static_cast<unsigned>((a.M + groups - 1) / groups)), block(tpr, groups);
+    const bool two = sizeof(TX) == 2 && !EDGE && tpr <= 256 && 2 * groups <= spread;
+    const int64_t rows = two ? 2 * groups : groups;
+    const dim3 grid(static_cast<unsigned>((a.M + rows - 1) / rows)), block(tpr, groups);
     auto run = [&](auto kernel) { return launch_pdl(kernel, grid, block, 0, stream, dim3(kNoCluster), X, a); };
-    if (ch == 1) return run(norm_forward_kernel<TX, EDGE, 1, 256, 6>);
-    if (ch == 2) return run(norm_forward_kernel<TX, EDGE, 2, 256, 5>);
-    if (tpr <= 256) return run(norm_forward_kernel<TX, EDGE, 4, 256, sizeof(TX) == 2 && !EDGE ? 5 : 4>);
-    return run(norm_forward_kernel<TX, EDGE, 4, kMaxThreads, 1>);
+    if constexpr (sizeof(TX) == 2 && !EDGE) {
+        if (two) {
+            if (ch == 1) return run(norm_forward_kernel<TX, EDGE, 1, 2, 256, 5>);
+            if (ch == 2) return run(norm_forward_kernel<TX, EDGE, 2, 2, 256, 5>);
+            return run(norm_forward_kernel<TX, EDGE, 4, 2, 256, 4>);
+        }
+    }
+    if (ch == 1) return run(norm_forward_kernel<TX, EDGE, 1, 1, 256, 6>);
+    if (ch == 2) return run(norm_forward_kernel<TX, EDGE, 2, 1, 256, 5>);
+    if (tpr <= 256) return run(norm_forward_kernel<TX, EDGE, 4, 1, 256, 4>);
+    return run(norm_forward_kernel<TX, EDGE, 4, 1, kMaxThreads, 1>);
 }
 
 template <typename TX>
@@ -864,7 +914,7 @@ Plan plan_of(int64_t M, int64_t K, int ex, int ed) {
 
 size_t smem_of(const Plan& p) {
     size_t ring = static_cast<size_t>(p.s.stages) * (p.s.slot_x + p.s.slot_d);
-    const size_t cols = static_cast<size_t>(2) * p.s.slice * sizeof(float);  // column sums
+    const size_t cols = static_cast<size_t>(2) * p.s.groups * p.s.slice * sizeof(float);  // column sums
     if (ring < cols) ring = cols;
     return ((sizeof(Control) + 127) & ~size_t(127)) + ring;
 }
