@@ -59,71 +59,111 @@ __device__ __forceinline__ uint32_t codes4(const float (&v)[4], float ratio) {
 
 // The first n of four codes; the others (the padding behind a row's end) are zero whatever
 // the block's scale.
-__device__ __forceinline__ uint32_t keep(uint32_t codes, int64_t n) {
-    return n >= 4 ? codes : n <= 0 ? 0u : codes & ((1u << (8 * static_cast<int>(n))) - 1u);
+__device__ __forceinline__ uint32_t keep(uint32_t codes, int n) {
+    return n >= 4 ? codes : n <= 0 ? 0u : codes & ((1u << (8 * n)) - 1u);
 }
 
-// Elements k .. k+3 of a row of K, zeros past its end.  VEC: K % 4 == 0 (k is), so the four
-// are there or not together and lie on their own alignment.
-template <bool VEC>
-__device__ __forceinline__ void load4(const float* row, int64_t k, int64_t K, float (&v)[4]) {
-    if constexpr (VEC) {
-        float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (k < K) a = __ldg(reinterpret_cast<const float4*>(row + k));
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = k + i < K ? __ldg(row + k + i) : 0.0f;
+// Elements k .. k+3 of a row of K as they lie in memory, zeros past its end (all bits zero is a
+// zero in either type).  Loading and converting are apart so that a thread's loads are all on
+// their way before the first is needed.  VEC: K % 4 == 0 (k is), so the four are there or not
+// together and lie on their own alignment.
+template <typename T>
+struct Raw4;
+template <>
+struct Raw4<float> {
+    float4 a;
+    __device__ __forceinline__ void clear() { a = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
+    template <bool VEC>
+    __device__ __forceinline__ void load(const float* row, int k, int K) {
+        clear();
+        if constexpr (VEC) {
+            if (k < K) a = __ldg(reinterpret_cast<const float4*>(row + k));
+        } else {
+            if (k < K) a.x = __ldg(row + k);
+            if (k + 1 < K) a.y = __ldg(row + k + 1);
+            if (k + 2 < K) a.z = __ldg(row + k + 2);
+            if (k + 3 < K) a.w = __ldg(row + k + 3);
+        }
     }
-}
-template <bool VEC>
-__device__ __forceinline__ void load4(const __nv_bfloat16* row, int64_t k, int64_t K, float (&v)[4]) {
-    if constexpr (VEC) {
-        uint2 a = make_uint2(0u, 0u);
-        if (k < K) a = __ldg(reinterpret_cast<const uint2*>(row + k));
-        v[0] = __uint_as_float(a.x << 16), v[1] = __uint_as_float(a.x & 0xFFFF0000u);
-        v[2] = __uint_as_float(a.y << 16), v[3] = __uint_as_float(a.y & 0xFFFF0000u);
-    } else {
+    __device__ __forceinline__ void values(float (&v)[4]) const { v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w; }
+};
+template <>
+struct Raw4<__nv_bfloat16> {
+    uint16_t h[4];
+    __device__ __forceinline__ void clear() { h[0] = h[1] = h[2] = h[3] = 0; }
+    template <bool VEC>
+    __device__ __forceinline__ void load(const __nv_bfloat16* row, int k, int K) {
+        const uint16_t* p = reinterpret_cast<const uint16_t*>(row + k);
+        if constexpr (VEC) {
+            uint2 a = make_uint2(0u, 0u);
+            if (k < K) a = __ldg(reinterpret_cast<const uint2*>(p));
+            *reinterpret_cast<uint2*>(h) = a;
+        } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = k + i < K ? __bfloat162float(row[k + i]) : 0.0f;
+            for (int i = 0; i < 4; ++i) h[i] = k + i < K ? __ldg(p + i) : uint16_t(0);
+        }
     }
-}
+    __device__ __forceinline__ void values(float (&v)[4]) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(static_cast<uint32_t>(h[i]) << 16);
+    }
+};
 
 __device__ __forceinline__ float absmax4(const float (&v)[4]) {
     return max_nan(max_nan(fabsf(v[0]), fabsf(v[1])), max_nan(fabsf(v[2]), fabsf(v[3])));
 }
 
 // ------------------------------------------------------------------ rows alone --
-// One warp per group of 128, four elements a lane (a warp's load is the whole group:
-// 256 or 512 neighbouring bytes, its store 128); four groups in flight per warp.
-constexpr int kU = 4;
+// A warp takes kU groups, four elements a lane (a load is a whole group: 256 or 512
+// neighbouring bytes, a store 128): 2^LG neighbouring groups of each of kU / 2^LG rows.  The
+// two quotients of a scale cost more instructions than the rest of its group, so lane u
+// computes those of group u for the whole warp.
+constexpr int kU = 8;
 constexpr int kRowWarps = 8;
 
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(32 * kRowWarps)
+template <typename T, bool VEC, int LG>
+__global__ void __launch_bounds__(32 * kRowWarps, 5)
     fp8_quant_rows_kernel(const T* __restrict__ X, int64_t M, int64_t K, int64_t pitch, float eps,
-                          uint8_t* __restrict__ q, float* __restrict__ s, int warps_per_row) {
+                          uint8_t* __restrict__ q, float* __restrict__ s, uint32_t spans) {
     pdl_wait_then_release();
+    constexpr int kAcross = 1 << LG, kRows = kU >> LG;
     const int lane = threadIdx.x;
-    const int rows = kRowWarps / warps_per_row;
-    const int64_t m = static_cast<int64_t>(blockIdx.x) * rows + threadIdx.y / warps_per_row;
-    if (m >= M) return;
-    const int64_t G = (K + kG - 1) / kG;
-    const T* row = X + m * K;
-    for (int64_t g0 = (static_cast<int64_t>(blockIdx.y) * warps_per_row + threadIdx.y % warps_per_row) * kU; g0 < G;
-         g0 += static_cast<int64_t>(gridDim.y) * warps_per_row * kU) {
-        float v[kU][4];
+    // warps: `spans` of them side by side cover a row
+    const uint32_t warp = blockIdx.x * kRowWarps + threadIdx.y;
+    const int64_t m0 = static_cast<int64_t>(warp / spans) * kRows;
+    const int64_t g0 = static_cast<int64_t>(warp % spans) * kAcross;
+    if (m0 >= M) return;
+    const int rows = M - m0 < kRows ? static_cast<int>(M - m0) : kRows;
+    // what is left of a row from the warp's first group on, at most a span and a bit
+    const int64_t rest = K - g0 * kG;
+    const int n = rest < 2 * kAcross * kG ? static_cast<int>(rest) : 2 * kAcross * kG;
+    const T* x0 = X + m0 * K + g0 * kG;
+    Raw4<T> x[kU];
 #pragma unroll
-        for (int u = 0; u < kU; ++u) load4<VEC>(row, (g0 + u) * kG + 4 * lane, K, v[u]);
+    for (int u = 0; u < kU; ++u)
+        x[u].template load<VEC>(x0 + (u / kAcross) * K, u % kAcross * kG + 4 * lane, u / kAcross < rows ? n : 0);
+    float absmax = 0.0f;
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            const int64_t g = g0 + u;
-            if (g >= G) break;
-            const Scale sc = scale_of(warp_absmax(absmax4(v[u])), eps);
-            const int64_t k = g * kG + 4 * lane;
-            if (k < pitch) *reinterpret_cast<uint32_t*>(q + m * pitch + k) = keep(codes4(v[u], sc.ratio), K - k);
-            if (lane == 0) s[g * M + m] = sc.d;
-        }
+    for (int u = 0; u < kU; ++u) {
+        float v[4];
+        x[u].values(v);
+        const float m = warp_absmax(absmax4(v));
+        if (lane == u) absmax = m;
+    }
+    const Scale mine = scale_of(absmax, eps);
+    if (lane < kU && lane / kAcross < rows && lane % kAcross * kG < n)
+        s[(g0 + lane % kAcross) * M + m0 + lane / kAcross] = mine.d;
+    uint8_t* q0 = q + m0 * pitch + g0 * kG + 4 * lane;
+    const int room = n + static_cast<int>(pitch - K);  // with the row's padding
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+        const float ratio = __shfl_sync(0xFFFFFFFFu, mine.ratio, u);
+        const int k = u % kAcross * kG + 4 * lane;
+        float v[4];
+        x[u].values(v);
+        if (u / kAcross < rows && k < room)
+            *reinterpret_cast<uint32_t*>(q0 + (u / kAcross) * pitch + u % kAcross * kG) =
+                keep(codes4(v, ratio), n - k);
     }
 }
 
@@ -131,10 +171,10 @@ __global__ void __launch_bounds__(32 * kRowWarps)
 // 16 warps hold a tile in registers: warp w rows 8 w .. 8 w + 7, lane l columns 4 l .. 4 l + 3
 // (a load is a whole row of the tile).  Row groups are reduced inside a warp, column groups
 // and blocks over the warps through shared memory.  Transposed codes are turned in shared
-// memory (a thread's eight rows of a column are eight neighbouring bytes there) and leave
-// as 16-byte pieces of 128-byte runs.
+// memory (a thread's eight rows of a column are eight neighbouring bytes there; the sixteen
+// eight-byte units of a column are swizzled by the lane that writes them, so that neither
+// side has bank conflicts) and leave as 16-byte pieces of 128-byte runs.
 constexpr int kTileWarps = 16;
-constexpr int kTPitch = kG + 16;  // bytes of a column's codes in shared memory
 
 struct TileArgs {
     int64_t M, K, tiles_k;
@@ -151,20 +191,21 @@ __global__ void __launch_bounds__(32 * kTileWarps)
     fp8_quant_tile_kernel(const T* __restrict__ X, const TileArgs a) {
     __shared__ float colmax[kTileWarps][kG];
     __shared__ float blockmax[kTileWarps];
-    __shared__ __align__(16) uint8_t turn[kG * kTPitch];
+    __shared__ __align__(16) uint8_t turn[kG * kG];
     pdl_wait_then_release();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t tm = blockIdx.x / a.tiles_k, tk = blockIdx.x % a.tiles_k;
     const int64_t m0 = tm * kG + 8 * warp, k0 = tk * kG + 4 * lane;
+    // rows and columns of the matrix from this thread's first on, at most the tile's
+    const int rows = a.M - m0 < 8 ? static_cast<int>(a.M - m0) : 8;
+    const int cols = a.K - tk * kG < kG ? static_cast<int>(a.K - tk * kG) : kG;
+    const T* x0 = X + m0 * a.K + tk * kG;
+    Raw4<T> x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i].template load<VEC>(x0 + i * a.K, 4 * lane, i < rows ? cols : 0);
     float v[8][4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        if (m0 + i < a.M) {
-            load4<VEC>(X + (m0 + i) * a.K, k0, a.K, v[i]);
-        } else {
-            v[i][0] = v[i][1] = v[i][2] = v[i][3] = 0.0f;
-        }
-    }
+    for (int i = 0; i < 8; ++i) x[i].values(v[i]);
     Scale sc[4];  // of this thread's columns (or of the block, four times)
     if constexpr (BLOCKS) {
         float mx = 0.0f;
@@ -199,35 +240,42 @@ __global__ void __launch_bounds__(32 * kTileWarps)
         sc[0].ratio = r.x, sc[1].ratio = r.y, sc[2].ratio = r.z, sc[3].ratio = r.w;
     }
     if (a.q != nullptr) {
+        Scale mine = sc[0];
+        if constexpr (!BLOCKS) {  // lane i computes the scale of row i for the warp
+            float absmax = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float m = warp_absmax(absmax4(v[i]));
+                if (lane == i) absmax = m;
+            }
+            mine = scale_of(absmax, a.eps);
+            if (lane < 8 && lane < rows) a.s[tk * a.M + m0 + lane] = mine.d;
+        }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            if (m0 + i >= a.M) break;
-            float ratio = sc[0].ratio;
-            if constexpr (!BLOCKS) {
-                const Scale r = scale_of(warp_absmax(absmax4(v[i])), a.eps);
-                ratio = r.ratio;
-                if (lane == 0) a.s[tk * a.M + m0 + i] = r.d;
-            }
+            const float ratio = BLOCKS ? mine.ratio : __shfl_sync(0xFFFFFFFFu, mine.ratio, i);
             // the last group's codes are padded with zeros to the pitch
-            if (k0 < a.pitch)
-                *reinterpret_cast<uint32_t*>(a.q + (m0 + i) * a.pitch + k0) = keep(codes4(v[i], ratio), a.K - k0);
+            if (i < rows && k0 < a.pitch)
+                *reinterpret_cast<uint32_t*>(a.q + (m0 + i) * a.pitch + k0) = keep(codes4(v[i], ratio), cols - 4 * lane);
         }
     }
     if (a.qt == nullptr) return;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const float lo[4] = {v[0][j], v[1][j], v[2][j], v[3][j]}, hi[4] = {v[4][j], v[5][j], v[6][j], v[7][j]};
-        *reinterpret_cast<uint2*>(turn + (4 * lane + j) * kTPitch + 8 * warp) =
-            make_uint2(keep(codes4(lo, sc[j].ratio), a.M - m0), keep(codes4(hi, sc[j].ratio), a.M - m0 - 4));
+        *reinterpret_cast<uint2*>(turn + (4 * lane + j) * kG + 8 * (warp ^ (lane & 15))) =
+            make_uint2(keep(codes4(lo, sc[j].ratio), rows), keep(codes4(hi, sc[j].ratio), rows - 4));
     }
     __syncthreads();
 #pragma unroll
     for (int p = threadIdx.x; p < kG * kG / 16; p += 32 * kTileWarps) {
         const int c = p / (kG / 16), piece = p % (kG / 16);
         const int64_t k = tk * kG + c, m = tm * kG + 16 * piece;
+        const int swizzle = (c >> 2) & 15;  // of the lane that wrote the column
+        const uint4 u = *reinterpret_cast<const uint4*>(turn + c * kG + 16 * (piece ^ (swizzle >> 1)));
         if (k < a.K && m < a.pitch_t)
             *reinterpret_cast<uint4*>(a.qt + k * a.pitch_t + m) =
-                *reinterpret_cast<const uint4*>(turn + c * kTPitch + 16 * piece);
+                (swizzle & 1) ? make_uint4(u.z, u.w, u.x, u.y) : u;
     }
 }
 
@@ -244,17 +292,25 @@ cudaError_t launch_tiles(const T* X, const TileArgs& a, cudaStream_t stream) {
 template <typename T>
 cudaError_t launch_rows(const T* X, int64_t M, int64_t K, float eps, uint8_t* q, float* s, cudaStream_t stream) {
     const int64_t G = (K + kG - 1) / kG;
-    int wpr = 1;
-    while (wpr < kRowWarps && static_cast<int64_t>(wpr) * kU < G) wpr *= 2;
-    const int rows = kRowWarps / wpr;
-    const int64_t y = (G + wpr * kU - 1) / (wpr * kU);
-    const dim3 grid(static_cast<unsigned>((M + rows - 1) / rows), static_cast<unsigned>(y < 65535 ? y : 65535));
-    const dim3 block(32, kRowWarps);
+    int lg = 0;  // groups of a row that a warp takes: 1, 2, 4 or 8
+    while (lg < 3 && (int64_t(1) << lg) < G) ++lg;
+    const int64_t spans = (G + (1 << lg) - 1) >> lg;
+    const int64_t rows = int64_t(kU) >> lg;
+    const int64_t blocks = ((M + rows - 1) / rows * spans + kRowWarps - 1) / kRowWarps;
+    if (blocks >= (int64_t(1) << 28)) return cudaErrorInvalidValue;  // 32-bit warp numbers
+    const dim3 grid(static_cast<unsigned>(blocks)), block(32, kRowWarps);
     const int64_t pitch = fp8_row_bytes(K);
-    return K % 4 == 0 ? launch_pdl(fp8_quant_rows_kernel<T, true>, grid, block, 0, stream, dim3(kNoCluster), X, M, K,
-                                   pitch, eps, q, s, wpr)
-                      : launch_pdl(fp8_quant_rows_kernel<T, false>, grid, block, 0, stream, dim3(kNoCluster), X, M, K,
-                                   pitch, eps, q, s, wpr);
+    auto run = [&](auto kernel) {
+        return launch_pdl(kernel, grid, block, 0, stream, dim3(kNoCluster), X, M, K, pitch, eps, q, s,
+                          static_cast<uint32_t>(spans));
+    };
+    const bool vec = K % 4 == 0;
+    switch (lg) {
+        case 0: return vec ? run(fp8_quant_rows_kernel<T, true, 0>) : run(fp8_quant_rows_kernel<T, false, 0>);
+        case 1: return vec ? run(fp8_quant_rows_kernel<T, true, 1>) : run(fp8_quant_rows_kernel<T, false, 1>);
+        case 2: return vec ? run(fp8_quant_rows_kernel<T, true, 2>) : run(fp8_quant_rows_kernel<T, false, 2>);
+        default: return vec ? run(fp8_quant_rows_kernel<T, true, 3>) : run(fp8_quant_rows_kernel<T, false, 3>);
+    }
 }
 
 }  // namespace

@@ -290,8 +290,8 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_forward_kernel(const TX*
         }
     }
     const float2 both = row_sum(q[0], R > 1 ? q[R - 1] : 0.0f);
-    rstd[0] = 1.0f / sqrtf(both.x * a.inv_k + a.eps);
-    if constexpr (R > 1) rstd[1] = 1.0f / sqrtf(both.y * a.inv_k + a.eps);
+    rstd[0] = __frsqrt_rn(fmaf(both.x, a.inv_k, a.eps));
+    if constexpr (R > 1) rstd[1] = __frsqrt_rn(fmaf(both.y, a.inv_k, a.eps));
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
         float w[kE], b[kE];
@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_forward_long_kernel(const TX
         const float d = to_f32(row[k]) - mu;
         v = fmaf(d, d, v);
     }
-    const float r = 1.0f / sqrtf(row_sum(v, 0.0f).x * a.inv_k + a.eps);
+    const float r = __frsqrt_rn(fmaf(row_sum(v, 0.0f).x, a.inv_k, a.eps));
     for (int64_t k = t; k < a.K; k += tpr) {
         float y = (to_f32(row[k]) - mu) * r;
         if (a.w != nullptr) y *= __ldg(a.w + k);
@@ -575,30 +575,31 @@ __global__ void __launch_bounds__(CH == 1 ? 800 : 640)
         float w[CH][kE];
 #pragma unroll
         for (int c = 0; c < CH; ++c) load_vector<EDGE>(a.w, 1.0f, pl.k0 + (c * tpr + t) * kE - skip, mask[c], w[c]);
+        // where the thread's chunks are in a slot: the same in every batch (see Shape)
+        const int64_t row0 = pl.first * s.K + pl.k0;
+        const int at = static_cast<int>((pl.first + pl.group) * s.K + pl.k0 - skip - (row0 & ~int64_t(kE - 1))) + t * kE;
+        int64_t flat = (pl.first + pl.group) * s.K + pl.k0 - skip + t * kE;  // of chunk 0, in the matrix
+        const int64_t flat_step = pl.step * s.K;
+        // values converted once with one chunk; with two that costs more (123 -> 133 us for 8192 x
+        // 8640 RMS), and the raw chunk is converted in each pass
+        constexpr bool kOnce = CH == 1;
         int stage = 0;
         uint32_t phase = 0;
-        for (int64_t m0 = pl.first; m0 < s.M; m0 += pl.step) {
+        for (int64_t m = pl.first + pl.group; m - pl.group < s.M; m += pl.step, flat += flat_step) {
             if (!mbar_wait_bounded(smem_u32(&pl.ctl->full[stage]), phase, &pl.ctl->abort)) break;
-            const int64_t m = m0 + pl.group;
             const bool live = m < s.M;
-            const int64_t flat0 = m * s.K + pl.k0 - skip;
+            const uint8_t* slot = pl.ring + stage * (s.slot_x + s.slot_d);
             Raw<TX> x[CH];
             Raw<TD> d[CH];
-            if (live) {
-                int64_t begin, end;
-                pl.span(s, m0, begin, end);
-                const uint8_t* slot = pl.ring + stage * (s.slot_x + s.slot_d);
-                const int at = static_cast<int>(flat0 - begin) + t * kE;
 #pragma unroll
-                for (int c = 0; c < CH; ++c) {
-                    const int i = at + c * tpr * kE;
-                    if (mask[c].any() && (!EDGE || i < static_cast<int>(end - begin))) {
-                        x[c].load(reinterpret_cast<const TX*>(slot) + i);
-                        d[c].load(reinterpret_cast<const TD*>(slot + s.slot_x) + i);
-                    } else {
-                        x[c].clear();
-                        d[c].clear();
-                    }
+            for (int c = 0; c < CH; ++c) {
+                const int i = at + c * tpr * kE;
+                if (live && mask[c].any() && (!EDGE || flat + (c * tpr + 1) * kE <= total)) {
+                    x[c].load(reinterpret_cast<const TX*>(slot) + i);
+                    d[c].load(reinterpret_cast<const TD*>(slot + s.slot_x) + i);
+                } else {
+                    x[c].clear();
+                    d[c].clear();
                 }
             }
             __syncwarp();
@@ -609,23 +610,30 @@ __global__ void __launch_bounds__(CH == 1 ? 800 : 640)
             }
             if (!live) continue;  // rows of a batch past the last one: the whole group skips
             // the values of chunk c, zero where they are not the row's
-            auto values = [&](int c, float(&xv)[kE], float(&dv)[kE]) {
-                if constexpr (EDGE) {
-                    const int64_t flat = flat0 + static_cast<int64_t>(c * tpr + t) * kE;
-                    if (mask[c].any() && flat + kE > total) {
-                        load_flat(X, flat, total, xv);  // the matrix's last chunk
-                        load_flat(dY, flat, total, dv);
-                    } else {
+            auto convert = [&](int c, float(&xv)[kE], float(&dv)[kE]) {
 #pragma unroll
-                        for (int e = 0; e < kE; ++e) xv[e] = x[c][e], dv[e] = d[c][e];
+                for (int e = 0; e < kE; ++e) xv[e] = x[c][e], dv[e] = d[c][e];
+                if constexpr (EDGE) {
+                    if (mask[c].any() && flat + (c * tpr + 1) * kE > total) {
+                        load_flat(X, flat + c * tpr * kE, total, xv);  // the matrix's last chunk
+                        load_flat(dY, flat + c * tpr * kE, total, dv);
                     }
                     if (!mask[c].all())
 #pragma unroll
                         for (int e = 0; e < kE; ++e)
                             if (!mask[c].has(e)) xv[e] = dv[e] = 0.0f;
-                } else {
+                }
+            };
+            float xs[kOnce ? CH : 1][kE], ds[kOnce ? CH : 1][kE];
+            if constexpr (kOnce)
 #pragma unroll
-                    for (int e = 0; e < kE; ++e) xv[e] = x[c][e], dv[e] = d[c][e];
+                for (int c = 0; c < CH; ++c) convert(c, xs[c], ds[c]);
+            auto values = [&](int c, float(&xv)[kE], float(&dv)[kE]) {
+                if constexpr (kOnce) {
+#pragma unroll
+                    for (int e = 0; e < kE; ++e) xv[e] = xs[c][e], dv[e] = ds[c][e];
+                } else {
+                    convert(c, xv, dv);
                 }
             };
             float mu = 0.0f, c2 = 0.0f;
@@ -659,7 +667,7 @@ __global__ void __launch_bounds__(CH == 1 ? 800 : 640)
                 }
             }
             const float2 both = row_sum(v, gx);
-            const float r = 1.0f / sqrtf(both.x * a.inv_k + a.eps);
+            const float r = __frsqrt_rn(fmaf(both.x, a.inv_k, a.eps));
             const float c1 = both.y * a.inv_k * r;
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
@@ -669,11 +677,11 @@ __global__ void __launch_bounds__(CH == 1 ? 800 : 640)
 #pragma unroll
                 for (int e = 0; e < kE; ++e) {
                     const float n = (xv[e] - mu) * r;
-                    xv[e] = r * ((dv[e] * w[c][e] - c2) - n * c1);
                     dw[c][e] = fmaf(dv[e], n, dw[c][e]);
                     if constexpr (DB) db[c][e] += dv[e];
+                    xv[e] = r * fmaf(-n, c1, fmaf(dv[e], w[c][e], -c2));
                 }
-                store_flat(a.dx, a.dx_bf16, flat0 + static_cast<int64_t>(c * tpr + t) * kE, mask[c], xv);
+                store_flat(a.dx, a.dx_bf16, flat + c * tpr * kE, mask[c], xv);
             }
         }
     }
@@ -766,7 +774,7 @@ __global__ void __launch_bounds__(kMaxThreads)
         gx = fmaf(grad(k), x, gx);
     }
     const float2 both = row_sum(v, gx);
-    const float r = 1.0f / sqrtf(both.x * a.inv_k + a.eps);
+    const float r = __frsqrt_rn(fmaf(both.x, a.inv_k, a.eps));
     const float c1 = both.y * a.inv_k * r;
     for (int64_t k = t; k < a.K; k += tpr) {
         const float n = (to_f32(row[k]) - mu) * r;
