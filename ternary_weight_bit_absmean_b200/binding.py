@@ -12,8 +12,8 @@ allocate the output tensors with torch and call the entry points above.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import os
 
 import torch
@@ -308,32 +308,60 @@ def bitlinear_ste_backward_weight(dY, xq, s, gamma, dW, stream=None):
 
 
 # The norm and e4m3 calls run on the device of their tensors (all on one), whichever is
-# current, and on its current stream or the one given.
+# current, and on its current stream or the one given.  A serving loop makes them for single
+# tokens, where the host's time counts, so the common case (that device is current, no stream
+# given) takes no context manager.
 
 _FLOATS = {torch.float32: BL_OUT_F32, torch.bfloat16: BL_OUT_BF16}
 _E4M3 = torch.float8_e4m3fn
-_HERE_ALREADY = contextlib.nullcontext()
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _scope(stream, *tensors):
-    """A context in which the tensors' device, and `stream` if given, are current."""
-    device = None
+    """None if the tensors' device is current and no stream is given, else a context in which
+    their device, and `stream`, are current."""
+    index = None
     for t in tensors:
         if t is None:
             continue
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
             raise TypeError("every tensor must be a CUDA tensor")
-        if device is None:
-            device = t.device
-        elif t.device != device:
-            raise ValueError("tensors must be on one device, got %s and %s" % (device, t.device))
+        i = t.get_device()
+        if index is None:
+            index = i
+        elif i != index:
+            raise ValueError("tensors must be on one device, got cuda:%d and cuda:%d" % (index, i))
     if stream is None:
-        return _HERE_ALREADY if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+        return None if index == torch.cuda.current_device() else torch.cuda.device(index)
     if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
-    if stream.device != device:
-        raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, device))
+        stream = torch.cuda.ExternalStream(int(stream), device=index)
+    if stream.device.index != index:
+        raise ValueError("the stream is on %s, the tensors on cuda:%d" % (stream.device, index))
     return torch.cuda.stream(stream)
+
+
+def _scoped(call):
+    """Runs `call` in the scope of its tensors: everything passed to it that is one, and the
+    keyword argument `stream`, which the call itself then does without."""
+    @functools.wraps(call)
+    def run(*args, stream=None, **kwargs):
+        tensors = [a for a in args if isinstance(a, torch.Tensor)]
+        if kwargs:
+            tensors += [a for a in kwargs.values() if isinstance(a, torch.Tensor)]
+        if not tensors:
+            raise TypeError("%s takes CUDA tensors" % call.__name__)
+        scope = _scope(stream, *tensors)
+        if scope is None:
+            return call(*args, **kwargs)
+        with scope:
+            return call(*args, **kwargs)
+    return run
+
+
+def _here(t) -> int:
+    """The current stream of the tensor's device."""
+    return _raw_stream(t.get_device())
 
 
 def _float(t: torch.Tensor, name: str, shape=None):
@@ -358,54 +386,58 @@ def _blocks(n: int) -> int:
     return -(-n // 128)
 
 
-def bitlinear_norm_forward(X, norm_weight, norm_bias, kind, norm_eps, out, stream=None):
+def _up16(n: int) -> int:
+    return -(-n // 16) * 16
+
+
+@_scoped
+def bitlinear_norm_forward(X, norm_weight, norm_bias, kind, norm_eps, out):
     M, K = _matrix(X, "X")
-    with _scope(stream, X, norm_weight, norm_bias, out):
-        _check(lib().bitlinear_norm_forward(
-            *_float(X, "X"), _vec(norm_weight, "norm_weight", K), _vec(norm_bias, "norm_bias", K), M, K, int(kind),
-            float(norm_eps), *_float(out, "out", (M, K)), _stream(None)), "bitlinear_norm_forward")
+    _check(lib().bitlinear_norm_forward(
+        *_float(X, "X"), _vec(norm_weight, "norm_weight", K), _vec(norm_bias, "norm_bias", K), M, K, int(kind),
+        float(norm_eps), *_float(out, "out", (M, K)), _here(X)), "bitlinear_norm_forward")
 
 
 def bitlinear_norm_backward_workspace_size(M: int, K: int) -> int:
     return int(lib().bitlinear_norm_backward_workspace_size(int(M), int(K)))
 
 
-def bitlinear_norm_backward(dY, X, norm_weight, kind, norm_eps, dX, dweight, dbias, ws, err_word=None, stream=None):
+@_scoped
+def bitlinear_norm_backward(dY, X, norm_weight, kind, norm_eps, dX, dweight, dbias, ws, err_word=None):
     M, K = _matrix(X, "X")
-    with _scope(stream, X, dY, norm_weight, dX, dweight, dbias, ws, err_word):
-        _check(lib().bitlinear_norm_backward(
-            *_float(dY, "dY", (M, K)), *_float(X, "X"), _vec(norm_weight, "norm_weight", K), M, K, int(kind),
-            float(norm_eps), *_float(dX, "dX", (M, K)), _vec(dweight, "dweight", K), _vec(dbias, "dbias", K),
-            None if ws is None else _dev(ws, torch.uint8, "ws"), 0 if ws is None else ws.numel(),
-            _opt(err_word, "err_word"), _stream(None)),
-            "bitlinear_norm_backward")
+    _check(lib().bitlinear_norm_backward(
+        *_float(dY, "dY", (M, K)), *_float(X, "X"), _vec(norm_weight, "norm_weight", K), M, K, int(kind),
+        float(norm_eps), *_float(dX, "dX", (M, K)), _vec(dweight, "dweight", K), _vec(dbias, "dbias", K),
+        None if ws is None else _dev(ws, torch.uint8, "ws"), 0 if ws is None else ws.numel(),
+        _opt(err_word, "err_word"), _here(dY)),
+        "bitlinear_norm_backward")
 
 
 def bitlinear_fp8_row_bytes(K: int) -> int:
     return int(lib().bitlinear_fp8_row_bytes(int(K)))
 
 
-def bitlinear_fp8_quantize_act(X, eps, xq_out, s_out, xqt_out=None, st_out=None, stream=None):
+@_scoped
+def bitlinear_fp8_quantize_act(X, eps, xq_out, s_out, xqt_out=None, st_out=None):
     M, K = _matrix(X, "X")
-    with _scope(stream, X, xq_out, s_out, xqt_out, st_out):
-        _check(lib().bitlinear_fp8_quantize_act(
-            *_float(X, "X"), M, K, float(eps),
-            None if xq_out is None else _dev(xq_out, _E4M3, "xq_out", (M, bitlinear_fp8_row_bytes(K))),
-            None if s_out is None else _dev(s_out, torch.float32, "s_out", (_blocks(K), M)),
-            None if xqt_out is None else _dev(xqt_out, _E4M3, "xqt_out", (K, bitlinear_fp8_row_bytes(M))),
-            None if st_out is None else _dev(st_out, torch.float32, "st_out", (_blocks(M), K)), _stream(None)),
-            "bitlinear_fp8_quantize_act")
+    _check(lib().bitlinear_fp8_quantize_act(
+        *_float(X, "X"), M, K, float(eps),
+        None if xq_out is None else _dev(xq_out, _E4M3, "xq_out", (M, _up16(K))),
+        None if s_out is None else _dev(s_out, torch.float32, "s_out", (_blocks(K), M)),
+        None if xqt_out is None else _dev(xqt_out, _E4M3, "xqt_out", (K, _up16(M))),
+        None if st_out is None else _dev(st_out, torch.float32, "st_out", (_blocks(M), K)), _here(X)),
+        "bitlinear_fp8_quantize_act")
 
 
-def bitlinear_fp8_quantize_weights(W, eps, wq_out, s_out, wqt_out=None, stream=None):
+@_scoped
+def bitlinear_fp8_quantize_weights(W, eps, wq_out, s_out, wqt_out=None):
     N, K = _matrix(W, "W")
-    with _scope(stream, W, wq_out, s_out, wqt_out):
-        _check(lib().bitlinear_fp8_quantize_weights(
-            *_float(W, "W"), N, K, float(eps),
-            None if wq_out is None else _dev(wq_out, _E4M3, "wq_out", (N, bitlinear_fp8_row_bytes(K))),
-            _dev(s_out, torch.float32, "s_out", (_blocks(N), _blocks(K))),
-            None if wqt_out is None else _dev(wqt_out, _E4M3, "wqt_out", (K, bitlinear_fp8_row_bytes(N))),
-            _stream(None)), "bitlinear_fp8_quantize_weights")
+    _check(lib().bitlinear_fp8_quantize_weights(
+        *_float(W, "W"), N, K, float(eps),
+        None if wq_out is None else _dev(wq_out, _E4M3, "wq_out", (N, _up16(K))),
+        _dev(s_out, torch.float32, "s_out", (_blocks(N), _blocks(K))),
+        None if wqt_out is None else _dev(wqt_out, _E4M3, "wqt_out", (K, _up16(N))),
+        _here(W)), "bitlinear_fp8_quantize_weights")
 
 
 def _codes_of(left, right, names):
@@ -419,31 +451,31 @@ def _codes_of(left, right, names):
     return rows_l, rows_r, n
 
 
-def bitlinear_fp8_forward(xq, sx, wq, sw, out, err_word=None, stream=None):
+@_scoped
+def bitlinear_fp8_forward(xq, sx, wq, sw, out, err_word=None):
     M, N, K = _codes_of(xq, wq, ("xq", "wq"))
-    with _scope(stream, xq, sx, wq, sw, out, err_word):
-        _check(lib().bitlinear_fp8_forward(
-            _dev(xq, _E4M3, "xq"), _dev(sx, torch.float32, "sx", (_blocks(K), M)), _dev(wq, _E4M3, "wq"),
-            _dev(sw, torch.float32, "sw", (_blocks(N), _blocks(K))), M, N, K, *_float(out, "out", (M, N)),
-            _opt(err_word, "err_word"), _stream(None)), "bitlinear_fp8_forward")
+    _check(lib().bitlinear_fp8_forward(
+        _dev(xq, _E4M3, "xq"), _dev(sx, torch.float32, "sx", (_blocks(K), M)), _dev(wq, _E4M3, "wq"),
+        _dev(sw, torch.float32, "sw", (_blocks(N), _blocks(K))), M, N, K, *_float(out, "out", (M, N)),
+        _opt(err_word, "err_word"), _here(xq)), "bitlinear_fp8_forward")
 
 
-def bitlinear_fp8_backward_input(dyq, sdy, wqt, sw, dX, err_word=None, stream=None):
+@_scoped
+def bitlinear_fp8_backward_input(dyq, sdy, wqt, sw, dX, err_word=None):
     M, K, N = _codes_of(dyq, wqt, ("dyq", "wqt"))
-    with _scope(stream, dyq, sdy, wqt, sw, dX, err_word):
-        _check(lib().bitlinear_fp8_backward_input(
-            _dev(dyq, _E4M3, "dyq"), _dev(sdy, torch.float32, "sdy", (_blocks(N), M)), _dev(wqt, _E4M3, "wqt"),
-            _dev(sw, torch.float32, "sw", (_blocks(N), _blocks(K))), M, N, K, *_float(dX, "dX", (M, K)),
-            _opt(err_word, "err_word"), _stream(None)), "bitlinear_fp8_backward_input")
+    _check(lib().bitlinear_fp8_backward_input(
+        _dev(dyq, _E4M3, "dyq"), _dev(sdy, torch.float32, "sdy", (_blocks(N), M)), _dev(wqt, _E4M3, "wqt"),
+        _dev(sw, torch.float32, "sw", (_blocks(N), _blocks(K))), M, N, K, *_float(dX, "dX", (M, K)),
+        _opt(err_word, "err_word"), _here(dyq)), "bitlinear_fp8_backward_input")
 
 
-def bitlinear_fp8_backward_weight(dyqt, sdyt, xqt, sxt, dW, err_word=None, stream=None):
+@_scoped
+def bitlinear_fp8_backward_weight(dyqt, sdyt, xqt, sxt, dW, err_word=None):
     N, K, M = _codes_of(dyqt, xqt, ("dyqt", "xqt"))
-    with _scope(stream, dyqt, sdyt, xqt, sxt, dW, err_word):
-        _check(lib().bitlinear_fp8_backward_weight(
-            _dev(dyqt, _E4M3, "dyqt"), _dev(sdyt, torch.float32, "sdyt", (_blocks(M), N)), _dev(xqt, _E4M3, "xqt"),
-            _dev(sxt, torch.float32, "sxt", (_blocks(M), K)), M, N, K, *_float(dW, "dW", (N, K)),
-            _opt(err_word, "err_word"), _stream(None)), "bitlinear_fp8_backward_weight")
+    _check(lib().bitlinear_fp8_backward_weight(
+        _dev(dyqt, _E4M3, "dyqt"), _dev(sdyt, torch.float32, "sdyt", (_blocks(M), N)), _dev(xqt, _E4M3, "xqt"),
+        _dev(sxt, torch.float32, "sxt", (_blocks(M), K)), M, N, K, *_float(dW, "dW", (N, K)),
+        _opt(err_word, "err_word"), _here(dyqt)), "bitlinear_fp8_backward_weight")
 
 
 # ----------------------------------------------------------- allocating helpers --
@@ -519,78 +551,79 @@ def ste_backward(dY, packed, xq, s, gamma, stream=None):
     return dX, dW
 
 
+# The helpers below take `stream` too (_scoped), and call the entry points' bodies directly:
+# their own arguments have been looked at, and what they allocate is on the same device and,
+# with a stream, belongs to it.
+
+@_scoped
 def norm_forward(X: torch.Tensor, norm_weight=None, norm_bias=None, kind=BL_NORM_RMS, norm_eps: float = 1e-5,
-                 out_dtype=None, stream=None):
+                 out_dtype=None):
     """RMSNorm / LayerNorm(X) [M, K] of an fp32 or bf16 CUDA matrix, as out_dtype (X's by default)."""
-    with _scope(stream, X):
-        out = torch.empty(X.shape, dtype=out_dtype or X.dtype, device=X.device)
-        bitlinear_norm_forward(X, norm_weight, norm_bias, kind, norm_eps, out)
+    out = X.new_empty(X.shape, dtype=out_dtype or X.dtype)
+    bitlinear_norm_forward.__wrapped__(X, norm_weight, norm_bias, kind, norm_eps, out)
     return out
 
 
+@_scoped
 def norm_backward(dY: torch.Tensor, X: torch.Tensor, norm_weight=None, kind=BL_NORM_RMS, norm_eps: float = 1e-5,
-                  bias: bool = False, dx_dtype=None, stream=None, err_word=None):
+                  bias: bool = False, dx_dtype=None, err_word=None):
     """(dX [M, K], dweight [K] fp32, dbias [K] fp32) of norm_forward for the gradient dY at its
     result.  dX is dx_dtype (dY's type by default); dweight is None without a norm_weight,
     dbias unless `bias`."""
     M, K = _matrix(X, "X")
-    with _scope(stream, X, dY):
-        dX = torch.empty(M, K, dtype=dx_dtype or dY.dtype, device=X.device)
-        dw = torch.empty(K, dtype=torch.float32, device=X.device) if norm_weight is not None else None
-        db = torch.empty(K, dtype=torch.float32, device=X.device) if bias else None
-        n = bitlinear_norm_backward_workspace_size(M, K)
-        ws = torch.empty(n, dtype=torch.uint8, device=X.device) if n else None
-        bitlinear_norm_backward(dY, X, norm_weight, kind, norm_eps, dX, dw, db, ws, err_word)
+    dX = X.new_empty((M, K), dtype=dx_dtype or dY.dtype)
+    dw = X.new_empty(K, dtype=torch.float32) if norm_weight is not None else None
+    db = X.new_empty(K, dtype=torch.float32) if bias else None
+    n = bitlinear_norm_backward_workspace_size(M, K)
+    ws = X.new_empty(n, dtype=torch.uint8) if n else None
+    bitlinear_norm_backward.__wrapped__(dY, X, norm_weight, kind, norm_eps, dX, dw, db, ws, err_word)
     return dX, dw, db
 
 
-def fp8_quantize_act(X: torch.Tensor, eps: float = 1e-5, transposed: bool = False, stream=None):
+@_scoped
+def fp8_quantize_act(X: torch.Tensor, eps: float = 1e-5, transposed: bool = False):
     """(xq, sx) of an fp32 or bf16 CUDA matrix: e4m3 codes [M, K rounded up to 16] and one fp32
     scale per 128 elements of a row [ceil(K/128), M].  With `transposed` also (xqt, sxt), the
     codes [K, M rounded up to 16] with one scale per 128 elements of a column."""
     M, K = _matrix(X, "X")
-    with _scope(stream, X):
-        out = [torch.empty(M, bitlinear_fp8_row_bytes(K), dtype=_E4M3, device=X.device),
-               torch.empty(_blocks(K), M, dtype=torch.float32, device=X.device)]
-        if transposed:
-            out += [torch.empty(K, bitlinear_fp8_row_bytes(M), dtype=_E4M3, device=X.device),
-                    torch.empty(_blocks(M), K, dtype=torch.float32, device=X.device)]
-        bitlinear_fp8_quantize_act(X, eps, *out)
-    return tuple(out)
-
-
-def fp8_quantize_weights(W: torch.Tensor, eps: float = 1e-5, transposed: bool = False, stream=None):
-    """(wq, sw) of an fp32 or bf16 CUDA weight matrix: e4m3 codes [N, K rounded up to 16] and one
-    fp32 scale per 128 x 128 block.  With `transposed` also wqt, the codes [K, N rounded up to 16]."""
-    N, K = _matrix(W, "W")
-    with _scope(stream, W):
-        out = [torch.empty(N, bitlinear_fp8_row_bytes(K), dtype=_E4M3, device=W.device),
-               torch.empty(_blocks(N), _blocks(K), dtype=torch.float32, device=W.device)]
-        if transposed:
-            out.append(torch.empty(K, bitlinear_fp8_row_bytes(N), dtype=_E4M3, device=W.device))
-        bitlinear_fp8_quantize_weights(W, eps, *out)
-    return tuple(out)
-
-
-def fp8_forward(xq, sx, wq, sw, out_dtype=torch.float32, stream=None, err_word=None):
-    """y [M, N] = x w^T from the codes and scales of fp8_quantize_act and fp8_quantize_weights."""
-    with _scope(stream, xq):
-        out = torch.empty(xq.shape[0], wq.shape[0], dtype=out_dtype, device=xq.device)
-        bitlinear_fp8_forward(xq, sx, wq, sw, out, err_word)
+    out = (X.new_empty((M, _up16(K)), dtype=_E4M3), X.new_empty((_blocks(K), M), dtype=torch.float32))
+    if transposed:
+        out += (X.new_empty((K, _up16(M)), dtype=_E4M3), X.new_empty((_blocks(M), K), dtype=torch.float32))
+    bitlinear_fp8_quantize_act.__wrapped__(X, eps, *out)
     return out
 
 
-def fp8_backward_input(dyq, sdy, wqt, sw, out_dtype=torch.float32, stream=None, err_word=None):
+@_scoped
+def fp8_quantize_weights(W: torch.Tensor, eps: float = 1e-5, transposed: bool = False):
+    """(wq, sw) of an fp32 or bf16 CUDA weight matrix: e4m3 codes [N, K rounded up to 16] and one
+    fp32 scale per 128 x 128 block.  With `transposed` also wqt, the codes [K, N rounded up to 16]."""
+    N, K = _matrix(W, "W")
+    out = (W.new_empty((N, _up16(K)), dtype=_E4M3), W.new_empty((_blocks(N), _blocks(K)), dtype=torch.float32))
+    if transposed:
+        out += (W.new_empty((K, _up16(N)), dtype=_E4M3),)
+    bitlinear_fp8_quantize_weights.__wrapped__(W, eps, *out)
+    return out
+
+
+@_scoped
+def fp8_forward(xq, sx, wq, sw, out_dtype=torch.float32, err_word=None):
+    """y [M, N] = x w^T from the codes and scales of fp8_quantize_act and fp8_quantize_weights."""
+    out = sx.new_empty((xq.shape[0], wq.shape[0]), dtype=out_dtype)
+    bitlinear_fp8_forward.__wrapped__(xq, sx, wq, sw, out, err_word)
+    return out
+
+
+@_scoped
+def fp8_backward_input(dyq, sdy, wqt, sw, out_dtype=torch.float32, err_word=None):
     """dX [M, K] = dY w from the gradient's codes and the transposed weight codes."""
-    with _scope(stream, dyq):
-        dX = torch.empty(dyq.shape[0], wqt.shape[0], dtype=out_dtype, device=dyq.device)
-        bitlinear_fp8_backward_input(dyq, sdy, wqt, sw, dX, err_word)
+    dX = sdy.new_empty((dyq.shape[0], wqt.shape[0]), dtype=out_dtype)
+    bitlinear_fp8_backward_input.__wrapped__(dyq, sdy, wqt, sw, dX, err_word)
     return dX
 
 
-def fp8_backward_weight(dyqt, sdyt, xqt, sxt, out_dtype=torch.float32, stream=None, err_word=None):
+@_scoped
+def fp8_backward_weight(dyqt, sdyt, xqt, sxt, out_dtype=torch.float32, err_word=None):
     """dW [N, K] = dY^T x from the transposed codes of the gradient and the activations."""
-    with _scope(stream, dyqt):
-        dW = torch.empty(dyqt.shape[0], xqt.shape[0], dtype=out_dtype, device=dyqt.device)
-        bitlinear_fp8_backward_weight(dyqt, sdyt, xqt, sxt, dW, err_word)
+    dW = sdyt.new_empty((dyqt.shape[0], xqt.shape[0]), dtype=out_dtype)
+    bitlinear_fp8_backward_weight.__wrapped__(dyqt, sdyt, xqt, sxt, dW, err_word)
     return dW
