@@ -23,6 +23,8 @@
 // partial sums through distributed shared memory in a fixed order.  All waits are bounded
 // as in the ternary kernels; a block that gives up drains its copies and MMAs, sets
 // BL_ERRBIT_TIMEOUT and still takes part in the cluster barriers.
+#include <algorithm>
+#include <cmath>
 #include <cuda_bf16.h>
 #include <cstdint>
 #include <cuda.h>
@@ -106,23 +108,44 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
     }
 }
 
-__device__ __forceinline__ float ld_shared_cluster_f32(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ float4 ld_shared_cluster_v4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
     return v;
 }
 
-__device__ __forceinline__ void store_one(const Fp8Product& d, int64_t q, int64_t p, float v) {
-    if (d.out_bf16)
-        static_cast<__nv_bfloat16*>(d.out)[q * d.P + p] = __float2bfloat16_rn(v);
-    else
-        static_cast<float*>(d.out)[q * d.P + p] = v;
+// out[q, p .. p + 3].
+__device__ __forceinline__ void store_four(const Fp8Product& d, int64_t q, int64_t p, float4 v) {
+    if (p >= d.P) return;
+    const int64_t at = q * d.P + p;
+    if (d.P % 4 == 0) {
+        if (d.out_bf16) {
+            const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(d.out) + at) =
+                make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+        } else {
+            *reinterpret_cast<float4*>(static_cast<float*>(d.out) + at) = v;
+        }
+        return;
+    }
+    const float y[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (p + i >= d.P) break;
+        if (d.out_bf16)
+            static_cast<__nv_bfloat16*>(d.out)[at + i] = __float2bfloat16_rn(y[i]);
+        else
+            static_cast<float*>(d.out)[at + i] = y[i];
+    }
 }
 
 // grid: x = (tile, block of the cluster), tiles ordered with the Qm tiles of one Pm tile
 // next to each other (they read the same Pm rows, from L2 after the first).
 template <int BQ>
-__global__ void __launch_bounds__(Cfg<BQ>::kThreads)
+__global__ void __launch_bounds__(Cfg<BQ>::kThreads, BQ >= 128 ? 1 : 2)
     fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_p,
                     const Args a, const int nsplit) {
     using C = Cfg<BQ>;
@@ -280,39 +303,60 @@ __global__ void __launch_bounds__(Cfg<BQ>::kThreads)
             tc_fence_after();
             const float* sc = scales + slot * C::kSlotFloats;
             const uint64_t sp2 = pack_f32x2(sc[BQ + r], sc[BQ + r]);
-            uint32_t v[C::kCols / 16][16];
+            constexpr int kW = C::kCols < 32 ? C::kCols : 32;  // columns read at a time
 #pragma unroll
-            for (int c = 0; c < C::kCols / 16; ++c)
-                tmem_ld_32x32b_x16(tmem_base + lane_addr + static_cast<uint32_t>(buf * BQ + c_begin + 16 * c), v[c]);
+            for (int c = 0; c < C::kCols; c += kW) {
+                uint32_t v[kW];
+                const uint32_t addr = tmem_base + lane_addr + static_cast<uint32_t>(buf * BQ + c_begin + c);
+                if constexpr (kW == 32)
+                    tmem_ld_32x32b_x32(addr, v);
+                else
+                    tmem_ld_32x32b_x16(addr, v);
+                tmem_ld_wait_for(v);
+                if (c + kW == C::kCols) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(tempty(buf));
+                }
 #pragma unroll
-            for (int c = 0; c < C::kCols / 16; ++c) tmem_ld_wait_for(v[c]);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(tempty(buf));
-#pragma unroll
-            for (int j = 0; j < C::kCols / 4; ++j) {
-                const float4 s4 = *reinterpret_cast<const float4*>(sc + c_begin + 4 * j);
-                const uint32_t* w = &v[j / 4][4 * (j % 4)];
-                acc[2 * j] = fma_f32x2(pack_f32x2(__uint_as_float(w[0]), __uint_as_float(w[1])),
-                                       mul_f32x2(sp2, pack_f32x2(s4.x, s4.y)), acc[2 * j]);
-                acc[2 * j + 1] = fma_f32x2(pack_f32x2(__uint_as_float(w[2]), __uint_as_float(w[3])),
-                                           mul_f32x2(sp2, pack_f32x2(s4.z, s4.w)), acc[2 * j + 1]);
+                for (int j = 0; j < kW / 4; ++j) {
+                    const float4 s4 = *reinterpret_cast<const float4*>(sc + c_begin + c + 4 * j);
+                    uint64_t* o = &acc[c / 2 + 2 * j];
+                    o[0] = fma_f32x2(pack_f32x2(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1])),
+                                     mul_f32x2(sp2, pack_f32x2(s4.x, s4.y)), o[0]);
+                    o[1] = fma_f32x2(pack_f32x2(__uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3])),
+                                     mul_f32x2(sp2, pack_f32x2(s4.z, s4.w)), o[1]);
+                }
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(sempty(slot));
         }
         if (ok) {
-            // with a split, every stage of this block has been read (its last group is in
-            // the sums), so the partial sums may take the stages' place
+            float y[C::kCols];
 #pragma unroll
-            for (int j = 0; j < C::kCols; ++j) {
-                const float2 two = unpack_f32x2(acc[j / 2]);
-                const float y = j % 2 == 0 ? two.x : two.y;
-                if (nsplit > 1) {
-                    red[(c_begin + j) * kRows + r] = y;
+            for (int j = 0; j < C::kCols / 2; ++j) {
+                const float2 two = unpack_f32x2(acc[j]);
+                y[2 * j] = two.x;
+                y[2 * j + 1] = two.y;
+            }
+            if (nsplit > 1) {
+                // every stage of this block has been read (its last group is in the sums), so the
+                // partial sums may take the stages' place
+#pragma unroll
+                for (int j = 0; j < C::kCols; ++j) red[(c_begin + j) * kRows + r] = y[j];
+            } else if (p0 + r < a.d.P) {
+                const int64_t left = a.d.Q - q0 - c_begin, at = (q0 + c_begin) * a.d.P + p0 + r;
+                const int n = left < C::kCols ? static_cast<int>(left) : C::kCols;
+                if (a.d.out_bf16) {
+                    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.d.out) + at;
+#pragma unroll
+                    for (int j = 0; j < C::kCols; ++j)
+                        if (j < n) o[j * a.d.P] = __float2bfloat16_rn(y[j]);
                 } else {
-                    const int64_t q = q0 + c_begin + j, p = p0 + r;
-                    if (q < a.d.Q && p < a.d.P) store_one(a.d, q, p, y);
+                    float* o = static_cast<float*>(a.d.out) + at;
+#pragma unroll
+                    for (int j = 0; j < C::kCols; ++j)
+                        if (j < n) o[j * a.d.P] = y[j];
                 }
             }
         }
@@ -321,19 +365,27 @@ __global__ void __launch_bounds__(Cfg<BQ>::kThreads)
     tc_fence_before();
     __syncthreads();
     if (nsplit > 1) {
-        // every block's partial sums are in its shared memory: block b adds, for the rows
-        // q with q % nsplit == b, the sums of all blocks in their order
+        // every block's partial sums are in its shared memory: the blocks share out the columns,
+        // and a thread adds four neighbouring rows of Pm over the blocks, in their order, with
+        // all of its loads from the other blocks on their way together
         cluster_sync_all();
-        const int rr = threadIdx.x & (kRows - 1);
-        const int64_t p = p0 + rr;
+        const int share = (BQ + nsplit - 1) / nsplit;
+        const int64_t left = a.d.Q - q0;
+        int end = split * share + share;
+        if (end > BQ) end = BQ;
+        if (end > left) end = static_cast<int>(left);
         const uint32_t red_addr = smem_u32(red);
-        for (int j = split + nsplit * (threadIdx.x / kRows); j < BQ; j += nsplit * (C::kThreads / kRows)) {
-            const int64_t q = q0 + j;
-            if (q >= a.d.Q || p >= a.d.P) continue;
-            float sum = 0.0f;
-            for (int b = 0; b < nsplit; ++b)
-                sum += ld_shared_cluster_f32(mapa_shared(red_addr + 4u * (j * kRows + rr), b));
-            store_one(a.d, q, p, sum);
+        for (int u = split * share * (kRows / 4) + static_cast<int>(threadIdx.x); u < end * (kRows / 4);
+             u += C::kThreads) {
+            float4 v[kMaxCluster];
+#pragma unroll
+            for (int b = 0; b < kMaxCluster; ++b)
+                if (b < nsplit) v[b] = ld_shared_cluster_v4(mapa_shared(red_addr + 16u * u, b));
+            float4 sum = v[0];
+#pragma unroll
+            for (int b = 1; b < kMaxCluster; ++b)
+                if (b < nsplit) sum.x += v[b].x, sum.y += v[b].y, sum.z += v[b].z, sum.w += v[b].w;
+            store_four(a.d, q0 + u / (kRows / 4), p0 + u % (kRows / 4) * 4, sum);
         }
         // no block leaves while another may still read its shared memory
         cluster_sync_all();
@@ -353,26 +405,13 @@ int sm_count() {
 }
 
 template <int BQ>
-cudaError_t launch_bq(const Fp8Product& d, cudaStream_t stream) {
+cudaError_t launch_bq(const Fp8Product& d, int split, cudaStream_t stream) {
     using C = Cfg<BQ>;
     const int64_t tiles_p = (d.P + kRows - 1) / kRows, tiles_q = (d.Q + BQ - 1) / BQ;
     const int groups = static_cast<int>((d.C + kG - 1) / kG);
-    // the split with the fewest waves x (groups of a block + its start, reduction and
-    // stores, about eight groups' time)
-    const int64_t slots = static_cast<int64_t>(sm_count()) * (BQ >= 128 ? 1 : 2);
-    const int64_t tiles = tiles_p * tiles_q;
-    int64_t split = 1, best = -1;
-    for (int64_t sp = 1; sp <= kMaxCluster && sp <= groups; ++sp) {
-        const int64_t waves = (tiles * sp + slots - 1) / slots;
-        const int64_t cost = waves * ((groups + sp - 1) / sp + 8);
-        if (best < 0 || cost < best) {
-            best = cost;
-            split = sp;
-        }
-    }
-    const int64_t per = (groups + split - 1) / split;
+    const int per = (groups + split - 1) / split;
     split = (groups + per - 1) / per;  // every block has at least one group
-    if (tiles * split >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
+    if (tiles_p * tiles_q * split >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
     CUtensorMap tq, tp;
     if (!encode_tmap_u8_pitch(&tq, d.q, static_cast<uint64_t>(d.C), static_cast<uint64_t>(d.Q),
                               static_cast<uint64_t>(fp8_row_bytes(d.C)), kG, BQ) ||
@@ -384,22 +423,75 @@ cudaError_t launch_bq(const Fp8Product& d, cudaStream_t stream) {
         return cudaFuncSetAttribute(fp8_gemm_kernel<BQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
     });
     if (e != cudaSuccess) return e;
-    const Args a{d, groups, static_cast<int>(per), static_cast<int>(tiles_q)};
-    return launch_pdl(fp8_gemm_kernel<BQ>, dim3(static_cast<unsigned>(tiles * split)), dim3(C::kThreads),
+    const Args a{d, groups, per, static_cast<int>(tiles_q)};
+    return launch_pdl(fp8_gemm_kernel<BQ>, dim3(static_cast<unsigned>(tiles_p * tiles_q * split)), dim3(C::kThreads),
                       C::kSmemBytes, stream, split > 1 ? dim3(static_cast<unsigned>(split), 1, 1) : dim3(kNoCluster),
-                      tq, tp, a, static_cast<int>(split));
+                      tq, tp, a, split);
 }
 
 }  // namespace
 
-cudaError_t launch_fp8_product_pair(const Fp8Product& d, cudaStream_t stream);
+cudaError_t launch_fp8_product_pair(const Fp8Product& d, int tile_p, int sms, cudaStream_t stream);
+
+// Which kernel runs a product: the one with the least expected time, in microseconds.  The rates
+// come from timing both sides of every choice on rows 1 .. 2048 of six weight shapes (512 x 256
+// to 28672 x 2048): a block takes `group` per group of 128 as long as neither HBM (6.9 TB/s) nor
+// the L2 (9 TB/s into the SMs) limits all of them together, after a fixed time for launch, first
+// loads and stores, more when partial sums are joined over a cluster.
+namespace {
+
+double time_small(const Fp8Product& d, int bq, int split, int sms) {
+    const double groups = static_cast<double>((d.C + kG - 1) / kG);
+    const double tiles = static_cast<double>((d.P + kRows - 1) / kRows) * static_cast<double>((d.Q + bq - 1) / bq);
+    const double per = std::ceil(groups / split);
+    split = static_cast<int>(std::ceil(groups / per));
+    const int occupancy = bq >= 128 ? 1 : 2;
+    // a cluster's blocks share a GPC, whose SMs larger clusters fill less well
+    const double fill = split == 1 ? 1.0 : split <= 4 ? 0.92 : split <= 6 ? 0.845 : 0.757;
+    const double waves = std::ceil(tiles * split / std::floor(sms * fill * occupancy));
+    const double group = bq <= 32 ? 0.255 : bq == 64 ? 0.30 : 0.32;
+    const double fixed = split > 1 ? (bq == 16 ? 3.7 : bq == 32 ? 5.0 : bq == 64 ? 5.7 : 7.0)
+                                   : (bq == 16 ? 2.5 : bq == 32 ? 3.2 : bq == 64 ? 4.5 : 5.2);
+    // reads of Pm; fewer than one and a half blocks per SM draw about 12% less
+    const double hbm = static_cast<double>(d.P) * static_cast<double>(d.C) / (tiles * split < 1.5 * sms ? 6.2e6 : 6.9e6);
+    const double l2 = tiles * groups * (bq + kRows) * kG / 9.0e6;
+    return fixed + std::max(waves * per * group, std::max(hbm, l2)) + (waves - 1) * (occupancy == 2 ? 2.2 : 5.0);
+}
+
+double time_pair(const Fp8Product& d, int tp, int sms) {
+    const double groups = static_cast<double>((d.C + kG - 1) / kG);
+    const double tiles = static_cast<double>((d.P + tp - 1) / tp) * static_cast<double>((d.Q + 255) / 256);
+    const double rounds = std::ceil(tiles / (sms / 2));
+    const bool rows = d.p_shift == 0;  // both sides scaled by row: twice the arithmetic per sum
+    const double group = tp == 256 ? (rows ? 0.65 : 0.47) : 0.345;
+    return (tp == 256 ? 5.8 : 4.5) + rounds * (groups * group + (tp == 256 ? 1.1 : 0.3));
+}
+
+}  // namespace
 
 cudaError_t launch_fp8_product(const Fp8Product& d, cudaStream_t stream) {
-    if (d.Q > 128) return launch_fp8_product_pair(d, stream);
-    if (d.Q <= 16) return launch_bq<16>(d, stream);
-    if (d.Q <= 32) return launch_bq<32>(d, stream);
-    if (d.Q <= 64) return launch_bq<64>(d, stream);
-    return launch_bq<128>(d, stream);
+    const int sms = sm_count();
+    const int64_t groups = (d.C + kG - 1) / kG;
+    const int bq = d.Q <= 16 ? 16 : d.Q <= 32 ? 32 : d.Q <= 64 ? 64 : 128;
+    int split = 1;
+    double best = time_small(d, bq, 1, sms);
+    for (int s = 2; s <= kMaxCluster && s <= groups; ++s) {
+        const double t = time_small(d, bq, s, sms);
+        if (t < best) best = t, split = s;
+    }
+    int tile_p = 0;
+    if (d.Q > 64)
+        for (int tp = 128; tp <= 256; tp += 128) {
+            const double t = time_pair(d, tp, sms);
+            if (t < best) best = t, tile_p = tp;
+        }
+    if (tile_p != 0) return launch_fp8_product_pair(d, tile_p, sms, stream);
+    switch (bq) {
+        case 16: return launch_bq<16>(d, split, stream);
+        case 32: return launch_bq<32>(d, split, stream);
+        case 64: return launch_bq<64>(d, split, stream);
+        default: return launch_bq<128>(d, split, stream);
+    }
 }
 
 }  // namespace bl

@@ -40,21 +40,27 @@ bool encode_tmap_u8_pitch(CUtensorMap* map, const void* ptr, uint64_t inner, uin
 
 namespace {
 
-constexpr int kHalf = 128;  // rows of Qm and of Pm per CTA
-constexpr int kTile = 2 * kHalf;
+constexpr int kHalf = 128;  // rows of Qm per CTA
+constexpr int kTileQ = 2 * kHalf;
 constexpr int kG = 128;
 constexpr int kThreads = 384;
 constexpr int kWarpTma = 0, kWarpMma = 1, kWarpScale = 2, kWarpEpi = 4, kEpiWarps = 8;
-constexpr int kCols = kTile / (kEpiWarps / 4);  // columns of an epilogue thread
-constexpr int kOpBytes = kHalf * kG;  // one operand's half per stage: 16 KB
-constexpr int kStages = 6;
 constexpr int kSlots = 8;             // scale ring
-constexpr int kSlotFloats = kHalf + kTile;
 constexpr int kTurnBytes = 2048;      // of an epilogue warp: 32 rows x 64 bytes of output
-constexpr int kBars = 2 * kStages + 4 + 2 * kSlots + 1;
-constexpr int kSmemBytes =
-    1024 + kStages * 2 * kOpBytes + kEpiWarps * kTurnBytes + kSlots * kSlotFloats * 4 + 8 * kBars + 16;
-static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+
+// TP: columns of a tile (rows of Pm), 256 or 128.
+template <int TP>
+struct Cfg {
+    static constexpr int kCols = TP / (kEpiWarps / 4);  // columns of an epilogue thread
+    static constexpr int kQBytes = kHalf * kG, kPBytes = TP / 2 * kG;  // of a stage, per CTA
+    static constexpr int kStages = TP == 256 ? 5 : 7;
+    static constexpr int kBufs = 512 / TP;              // accumulators
+    static constexpr int kSlotFloats = kHalf + TP;
+    static constexpr int kBars = 2 * kStages + 2 * kBufs + 2 * kSlots + 1;
+    static constexpr int kSmemBytes = 1024 + kStages * (kQBytes + kPBytes) + kEpiWarps * kTurnBytes +
+                                      kSlots * kSlotFloats * 4 + 8 * kBars + 16;
+    static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+};
 // the first four warps give up registers for the epilogue's sums: 128 * 56 + 256 * 224 is the
 // 384 * 168 that the block is launched with
 constexpr int kRegsLaunch = 168, kRegsSmall = 56, kRegsEpi = 224;
@@ -70,13 +76,13 @@ struct Args {
 // Tiles in panels of kPanel tiles along q, p running inside a panel: the tiles in flight share
 // few rows of either operand, so both stay in L2.
 constexpr int kPanel = 8;
-__device__ __forceinline__ void tile_origin(const Args& a, int tile, int64_t& q0, int64_t& p0) {
+__device__ __forceinline__ void tile_origin(const Args& a, int tp, int tile, int64_t& q0, int64_t& p0) {
     const int panel = tile / (kPanel * a.tiles_p);
     const int rest = tile - panel * kPanel * a.tiles_p;
     const int left = a.tiles_q - panel * kPanel;
     const int high = left < kPanel ? left : kPanel;
-    q0 = static_cast<int64_t>(panel * kPanel + rest % high) * kTile;
-    p0 = static_cast<int64_t>(rest / high) * kTile;
+    q0 = static_cast<int64_t>(panel * kPanel + rest % high) * kTileQ;
+    p0 = static_cast<int64_t>(rest / high) * tp;
 }
 
 __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
@@ -102,7 +108,7 @@ __device__ __forceinline__ void add_scaled2(const uint32_t* v, uint64_t scale, f
 // A row's sums sit in one thread, so storing them from there would write 32 scattered pieces
 // per instruction; they are turned in shared memory (64 bytes of every row at a time, 16-byte
 // chunks swizzled so that neither side has bank conflicts) and leave as runs of 64 bytes.
-template <typename T>
+template <typename T, int kCols>
 __device__ __forceinline__ void store_rows(const Fp8Product& d, int64_t q, int64_t p, const float (&acc)[kCols],
                                            uint8_t* turn, int lane) {
     constexpr int kPer = 64 / static_cast<int>(sizeof(T));  // columns per round: 16 or 32
@@ -147,28 +153,29 @@ __device__ __forceinline__ void store_rows(const Fp8Product& d, int64_t q, int64
 }
 
 // ROWS: Pm is scaled by row (p_shift 0), else by blocks of 128 rows.
-template <bool ROWS>
+template <bool ROWS, int TP>
 __global__ void __launch_bounds__(kThreads, 1)
     fp8_gemm2_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_p,
                      const Args a) {
-    constexpr int ST = kStages;
+    using C = Cfg<TP>;
+    constexpr int ST = C::kStages, NB = C::kBufs, kCols = C::kCols;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t* gbase = smem_raw + (base - raw);
     const uint32_t sQ = base;
-    const uint32_t sP = sQ + ST * kOpBytes;
-    const uint32_t sTurn = sP + ST * kOpBytes;
+    const uint32_t sP = sQ + ST * C::kQBytes;
+    const uint32_t sTurn = sP + ST * C::kPBytes;
     const uint32_t sScale = sTurn + kEpiWarps * kTurnBytes;
-    const uint32_t sBar = sScale + kSlots * kSlotFloats * 4;
+    const uint32_t sBar = sScale + kSlots * C::kSlotFloats * 4;
     auto full = [&](int s) { return sBar + 8u * s; };               // even CTA: both CTAs' loads
     auto empty = [&](int s) { return sBar + 8u * (ST + s); };       // local: stage read by the MMAs
     auto tfull = [&](int b) { return sBar + 8u * (2 * ST + b); };   // local: accumulator holds a group
-    auto tempty = [&](int b) { return sBar + 8u * (2 * ST + 2 + b); };  // even CTA: read by both CTAs
-    auto sfull = [&](int s) { return sBar + 8u * (2 * ST + 4 + s); };
-    auto sempty = [&](int s) { return sBar + 8u * (2 * ST + 4 + kSlots + s); };
-    const uint32_t drain_bar = sBar + 8u * (kBars - 1);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + (sBar - base) + 8 * kBars);
+    auto tempty = [&](int b) { return sBar + 8u * (2 * ST + NB + b); };  // even CTA: read by both CTAs
+    auto sfull = [&](int s) { return sBar + 8u * (2 * ST + 2 * NB + s); };
+    auto sempty = [&](int s) { return sBar + 8u * (2 * ST + 2 * NB + kSlots + s); };
+    const uint32_t drain_bar = sBar + 8u * (C::kBars - 1);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + (sBar - base) + 8 * C::kBars);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const float* scales = reinterpret_cast<const float*>(gbase + (sScale - base));
 
@@ -182,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(full(s), 1);
             mbar_init(empty(s), 1);
         }
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < NB; ++b) {
             mbar_init(tfull(b), 1);
             mbar_init(tempty(b), 2 * kEpiWarps);
         }
@@ -217,19 +224,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             for (int tile = first; ok && tile < a.num_tiles; tile += step) {
                 int64_t q0, p0;
-                tile_origin(a, tile, q0, p0);
+                tile_origin(a, TP, tile, q0, p0);
                 const int qr = static_cast<int>(q0) + kHalf * static_cast<int>(rank);
-                const int pr = static_cast<int>(p0) + kHalf * static_cast<int>(rank);
+                const int pr = static_cast<int>(p0) + TP / 2 * static_cast<int>(rank);
                 for (int g = 0; g < a.groups; ++g) {
                     if (!mbar_wait_cluster_bounded(empty(stage), phase ^ 1u, abort_flag)) {
                         ok = false;
                         break;
                     }
                     if (elect_one()) {
-                        if (leader) mbar_arrive_expect_tx(full(stage), 4 * kOpBytes);
+                        if (leader) mbar_arrive_expect_tx(full(stage), 2 * (C::kQBytes + C::kPBytes));
                         const uint32_t bar = mapa_shared(full(stage), 0);
-                        tma_load_2d_pair(sQ + stage * kOpBytes, &tmap_q, bar, g * kG, qr);
-                        tma_load_2d_pair(sP + stage * kOpBytes, &tmap_p, bar, g * kG, pr);
+                        tma_load_2d_pair(sQ + stage * C::kQBytes, &tmap_q, bar, g * kG, qr);
+                        tma_load_2d_pair(sP + stage * C::kPBytes, &tmap_p, bar, g * kG, pr);
                     }
                     __syncwarp();
                     ++issued;
@@ -254,14 +261,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             for (int tile = first; ok && tile < a.num_tiles; tile += step) {
                 int64_t q0, p0;
-                tile_origin(a, tile, q0, p0);
+                tile_origin(a, TP, tile, q0, p0);
                 q0 += kHalf * static_cast<int>(rank);
                 for (int g = 0; g < a.groups; ++g) {
                     if (!mbar_wait_bounded(sempty(slot), phase ^ 1u, abort_flag)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t dst = sScale + static_cast<uint32_t>(slot * kSlotFloats * 4 + 4 * lane);
+                    const uint32_t dst = sScale + static_cast<uint32_t>(slot * C::kSlotFloats * 4 + 4 * lane);
                     const float* sq = a.d.sq + g * a.d.Q;
 #pragma unroll
                     for (int c = 0; c < kHalf / 32; ++c) {
@@ -270,10 +277,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     const float* sp = a.d.sp + g * a.d.sp_g;
 #pragma unroll
-                    for (int c = 0; c < (ROWS ? kTile / 32 : 1); ++c) {
-                        // by blocks: two of them, copied by lanes 0 and 1
-                        if (!ROWS && lane > 1) break;
-                        const int64_t row = p0 + (ROWS ? 32 * c + lane : kHalf * lane);
+                    for (int c = 0; c < (ROWS ? TP / 32 : 1); ++c) {
+                        // by blocks: one for each 128 columns, copied by the first lanes
+                        if (!ROWS && lane >= TP / 128) break;
+                        const int64_t row = p0 + (ROWS ? 32 * c + lane : 128 * lane);
                         const int64_t p = row < a.d.P ? row : a.d.P - 1;
                         cp_async4(dst + 4u * kHalf + 128u * c, sp + (p >> a.d.p_shift) * a.d.sp_p);
                     }
@@ -287,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             cp_async_wait_all();
         } else if (warp == kWarpMma && leader) {
             // ---------------------------------------------------------- MMA issuer --
-            constexpr uint32_t idesc = idesc_e4m3(kTile, kTile);
+            constexpr uint32_t idesc = idesc_e4m3(kTileQ, TP);
             int stage = 0, buf = 0;
             uint32_t phase = 0, bphase = 0;
             bool ok = true;
@@ -300,10 +307,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     tc_fence_after();
                     if (elect_one()) {
-                        const uint32_t qa = sQ + stage * kOpBytes, pa = sP + stage * kOpBytes;
+                        const uint32_t qa = sQ + stage * C::kQBytes, pa = sP + stage * C::kPBytes;
 #pragma unroll
                         for (int kk = 0; kk < kG / 32; ++kk)
-                            tc_mma_f8_pair(tmem_base + static_cast<uint32_t>(buf * kTile),
+                            tc_mma_f8_pair(tmem_base + static_cast<uint32_t>(buf * TP),
                                            smem_desc_sw128(qa + kk * 32), smem_desc_sw128(pa + kk * 32), idesc,
                                            kk != 0 ? 1u : 0u);
                         // the accumulator's readers are the ones being waited for
@@ -315,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         stage = 0;
                         phase ^= 1u;
                     }
-                    if (++buf == 2) {
+                    if (++buf == NB) {
                         buf = 0;
                         bphase ^= 1u;
                     }
@@ -349,14 +356,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ok = false;
                     break;
                 }
-                const float* sc = scales + slot * kSlotFloats;
-                const float fq = sc[r] * (ROWS ? 1.0f : sc[kHalf + block * kCols / kHalf]);
+                const float* sc = scales + slot * C::kSlotFloats;
+                const float fq = sc[r] * (ROWS ? 1.0f : sc[kHalf + block * kCols / 128]);
                 if (!mbar_wait_cluster_bounded(tfull(buf), bphase, abort_flag)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t addr = t_addr + static_cast<uint32_t>(buf * kTile);
+                const uint32_t addr = t_addr + static_cast<uint32_t>(buf * TP);
                 // the next 32 columns are on their way while these are scaled
                 uint32_t v2[2][32];
                 tmem_ld_32x32b_x32(addr, v2[0]);
@@ -393,20 +400,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                     slot = 0;
                     sphase ^= 1u;
                 }
-                if (++buf == 2) {
+                if (++buf == NB) {
                     buf = 0;
                     bphase ^= 1u;
                 }
             }
             if (!ok) break;
             int64_t q0, p0;
-            tile_origin(a, tile, q0, p0);
+            tile_origin(a, TP, tile, q0, p0);
             q0 += kHalf * static_cast<int>(rank) + 32 * quarter;
             p0 += kCols * block;
             if (a.d.out_bf16)
-                store_rows<__nv_bfloat16>(a.d, q0, p0, acc, turn, lane);
+                store_rows<__nv_bfloat16, kCols>(a.d, q0, p0, acc, turn, lane);
             else
-                store_rows<float>(a.d, q0, p0, acc, turn, lane);
+                store_rows<float, kCols>(a.d, q0, p0, acc, turn, lane);
         }
     }
 
@@ -420,35 +427,36 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0 && *abort_flag && a.d.err != nullptr) atomicOr(a.d.err, kErrBitTimeout);
 }
 
-template <bool ROWS>
-cudaError_t launch(const CUtensorMap& tq, const CUtensorMap& tp, const Args& a, int pairs, cudaStream_t stream) {
-    static PerContextOnce attr;
-    cudaError_t e = attr.run([] {
-        return cudaFuncSetAttribute(fp8_gemm2_kernel<ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-    });
-    if (e != cudaSuccess) return e;
-    return launch_pdl(fp8_gemm2_kernel<ROWS>, dim3(static_cast<unsigned>(2 * pairs)), dim3(kThreads), kSmemBytes,
-                      stream, dim3(2, 1, 1), tq, tp, a);
-}
-
-}  // namespace
-
-cudaError_t launch_fp8_product_pair(const Fp8Product& d, cudaStream_t stream) {
-    int dev = 0, sms = 148;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    const int64_t tiles_q = (d.Q + kTile - 1) / kTile, tiles_p = (d.P + kTile - 1) / kTile;
+template <bool ROWS, int TP>
+cudaError_t launch(const Fp8Product& d, int sms, cudaStream_t stream) {
+    using C = Cfg<TP>;
+    const int64_t tiles_q = (d.Q + kTileQ - 1) / kTileQ, tiles_p = (d.P + TP - 1) / TP;
     // tile numbers are 32-bit, with room for one more step of the grid
     if (tiles_q * tiles_p >= (int64_t(1) << 30)) return cudaErrorInvalidValue;
     CUtensorMap tq, tp;
     const uint64_t pitch = static_cast<uint64_t>(fp8_row_bytes(d.C));
     if (!encode_tmap_u8_pitch(&tq, d.q, static_cast<uint64_t>(d.C), static_cast<uint64_t>(d.Q), pitch, kG, kHalf) ||
-        !encode_tmap_u8_pitch(&tp, d.p, static_cast<uint64_t>(d.C), static_cast<uint64_t>(d.P), pitch, kG, kHalf))
+        !encode_tmap_u8_pitch(&tp, d.p, static_cast<uint64_t>(d.C), static_cast<uint64_t>(d.P), pitch, kG, TP / 2))
         return cudaErrorInvalidValue;
+    static PerContextOnce attr;
+    cudaError_t e = attr.run([] {
+        return cudaFuncSetAttribute(fp8_gemm2_kernel<ROWS, TP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    C::kSmemBytes);
+    });
+    if (e != cudaSuccess) return e;
     const Args a{d, static_cast<int>((d.C + kG - 1) / kG), static_cast<int>(tiles_q), static_cast<int>(tiles_p),
                  static_cast<int>(tiles_q * tiles_p)};
     const int pairs = a.num_tiles < sms / 2 ? a.num_tiles : sms / 2;
-    return d.p_shift == 0 ? launch<true>(tq, tp, a, pairs, stream) : launch<false>(tq, tp, a, pairs, stream);
+    return launch_pdl(fp8_gemm2_kernel<ROWS, TP>, dim3(static_cast<unsigned>(2 * pairs)), dim3(kThreads),
+                      C::kSmemBytes, stream, dim3(2, 1, 1), tq, tp, a);
+}
+
+}  // namespace
+
+cudaError_t launch_fp8_product_pair(const Fp8Product& d, int tile_p, int sms, cudaStream_t stream) {
+    if (tile_p == 256)
+        return d.p_shift == 0 ? launch<true, 256>(d, sms, stream) : launch<false, 256>(d, sms, stream);
+    return d.p_shift == 0 ? launch<true, 128>(d, sms, stream) : launch<false, 128>(d, sms, stream);
 }
 
 }  // namespace bl
