@@ -318,22 +318,23 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _scope(stream, *tensors):
-    """None if the tensors' device is current and no stream is given, else a context in which
-    their device, and `stream`, are current."""
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _scope(stream, tensors):
+    """A context in which the tensors' device, and `stream` if given, are current."""
     index = None
     for t in tensors:
-        if t is None:
-            continue
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        if not t.is_cuda:
             raise TypeError("every tensor must be a CUDA tensor")
-        i = t.get_device()
         if index is None:
-            index = i
-        elif i != index:
-            raise ValueError("tensors must be on one device, got cuda:%d and cuda:%d" % (index, i))
+            index = t.get_device()
+        elif t.get_device() != index:
+            raise ValueError("tensors must be on one device, got cuda:%d and cuda:%d" % (index, t.get_device()))
+    if index is None:
+        raise TypeError("no CUDA tensor given")
     if stream is None:
-        return None if index == torch.cuda.current_device() else torch.cuda.device(index)
+        return torch.cuda.device(index)
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=index)
     if stream.device.index != index:
@@ -346,15 +347,20 @@ def _scoped(call):
     keyword argument `stream`, which the call itself then does without."""
     @functools.wraps(call)
     def run(*args, stream=None, **kwargs):
-        tensors = [a for a in args if isinstance(a, torch.Tensor)]
-        if kwargs:
-            tensors += [a for a in kwargs.values() if isinstance(a, torch.Tensor)]
-        if not tensors:
-            raise TypeError("%s takes CUDA tensors" % call.__name__)
-        scope = _scope(stream, *tensors)
-        if scope is None:
-            return call(*args, **kwargs)
-        with scope:
+        if stream is None:
+            # the common case: every tensor on one device, which is current
+            index = None
+            for a in (*args, *kwargs.values()) if kwargs else args:
+                if isinstance(a, torch.Tensor):
+                    i = a.get_device()
+                    if index is None:
+                        index = i
+                    elif i != index:
+                        index = -1
+                        break
+            if index is not None and index >= 0 and index == _device():
+                return call(*args, **kwargs)
+        with _scope(stream, [a for a in (*args, *kwargs.values()) if isinstance(a, torch.Tensor)]):
             return call(*args, **kwargs)
     return run
 
@@ -364,16 +370,24 @@ def _here(t) -> int:
     return _raw_stream(t.get_device())
 
 
-def _float(t: torch.Tensor, name: str, shape=None):
+def _ptr(t, dtype, name: str, shape=None) -> int:
+    """_dev, with the usual case (nothing to complain about) decided by a few quick tests."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.is_contiguous() and (
+            shape is None or t.shape == shape):
+        return t.data_ptr()
+    return _dev(t, dtype, name, shape)
+
+
+def _float(t, name: str, shape=None):
     """(pointer, bl_dtype) of an fp32 or bf16 tensor."""
     kind = _FLOATS.get(t.dtype) if isinstance(t, torch.Tensor) else None
     if kind is None:
         raise TypeError("%s must be float32 or bfloat16" % name)
-    return _dev(t, t.dtype, name, shape), kind
+    return _ptr(t, t.dtype, name, shape), kind
 
 
 def _vec(t, name, K):
-    return None if t is None else _dev(t, torch.float32, name, (K,))
+    return None if t is None else _ptr(t, torch.float32, name, (K,))
 
 
 def _matrix(t, name):
@@ -408,7 +422,7 @@ def bitlinear_norm_backward(dY, X, norm_weight, kind, norm_eps, dX, dweight, dbi
     _check(lib().bitlinear_norm_backward(
         *_float(dY, "dY", (M, K)), *_float(X, "X"), _vec(norm_weight, "norm_weight", K), M, K, int(kind),
         float(norm_eps), *_float(dX, "dX", (M, K)), _vec(dweight, "dweight", K), _vec(dbias, "dbias", K),
-        None if ws is None else _dev(ws, torch.uint8, "ws"), 0 if ws is None else ws.numel(),
+        None if ws is None else _ptr(ws, torch.uint8, "ws"), 0 if ws is None else ws.numel(),
         _opt(err_word, "err_word"), _here(dY)),
         "bitlinear_norm_backward")
 
@@ -422,10 +436,10 @@ def bitlinear_fp8_quantize_act(X, eps, xq_out, s_out, xqt_out=None, st_out=None)
     M, K = _matrix(X, "X")
     _check(lib().bitlinear_fp8_quantize_act(
         *_float(X, "X"), M, K, float(eps),
-        None if xq_out is None else _dev(xq_out, _E4M3, "xq_out", (M, _up16(K))),
-        None if s_out is None else _dev(s_out, torch.float32, "s_out", (_blocks(K), M)),
-        None if xqt_out is None else _dev(xqt_out, _E4M3, "xqt_out", (K, _up16(M))),
-        None if st_out is None else _dev(st_out, torch.float32, "st_out", (_blocks(M), K)), _here(X)),
+        None if xq_out is None else _ptr(xq_out, _E4M3, "xq_out", (M, _up16(K))),
+        None if s_out is None else _ptr(s_out, torch.float32, "s_out", (_blocks(K), M)),
+        None if xqt_out is None else _ptr(xqt_out, _E4M3, "xqt_out", (K, _up16(M))),
+        None if st_out is None else _ptr(st_out, torch.float32, "st_out", (_blocks(M), K)), _here(X)),
         "bitlinear_fp8_quantize_act")
 
 
@@ -434,9 +448,9 @@ def bitlinear_fp8_quantize_weights(W, eps, wq_out, s_out, wqt_out=None):
     N, K = _matrix(W, "W")
     _check(lib().bitlinear_fp8_quantize_weights(
         *_float(W, "W"), N, K, float(eps),
-        None if wq_out is None else _dev(wq_out, _E4M3, "wq_out", (N, _up16(K))),
-        _dev(s_out, torch.float32, "s_out", (_blocks(N), _blocks(K))),
-        None if wqt_out is None else _dev(wqt_out, _E4M3, "wqt_out", (K, _up16(N))),
+        None if wq_out is None else _ptr(wq_out, _E4M3, "wq_out", (N, _up16(K))),
+        _ptr(s_out, torch.float32, "s_out", (_blocks(N), _blocks(K))),
+        None if wqt_out is None else _ptr(wqt_out, _E4M3, "wqt_out", (K, _up16(N))),
         _here(W)), "bitlinear_fp8_quantize_weights")
 
 
@@ -455,8 +469,8 @@ def _codes_of(left, right, names):
 def bitlinear_fp8_forward(xq, sx, wq, sw, out, err_word=None):
     M, N, K = _codes_of(xq, wq, ("xq", "wq"))
     _check(lib().bitlinear_fp8_forward(
-        _dev(xq, _E4M3, "xq"), _dev(sx, torch.float32, "sx", (_blocks(K), M)), _dev(wq, _E4M3, "wq"),
-        _dev(sw, torch.float32, "sw", (_blocks(N), _blocks(K))), M, N, K, *_float(out, "out", (M, N)),
+        _ptr(xq, _E4M3, "xq"), _ptr(sx, torch.float32, "sx", (_blocks(K), M)), _ptr(wq, _E4M3, "wq"),
+        _ptr(sw, torch.float32, "sw", (_blocks(N), _blocks(K))), M, N, K, *_float(out, "out", (M, N)),
         _opt(err_word, "err_word"), _here(xq)), "bitlinear_fp8_forward")
 
 
@@ -464,8 +478,8 @@ def bitlinear_fp8_forward(xq, sx, wq, sw, out, err_word=None):
 def bitlinear_fp8_backward_input(dyq, sdy, wqt, sw, dX, err_word=None):
     M, K, N = _codes_of(dyq, wqt, ("dyq", "wqt"))
     _check(lib().bitlinear_fp8_backward_input(
-        _dev(dyq, _E4M3, "dyq"), _dev(sdy, torch.float32, "sdy", (_blocks(N), M)), _dev(wqt, _E4M3, "wqt"),
-        _dev(sw, torch.float32, "sw", (_blocks(N), _blocks(K))), M, N, K, *_float(dX, "dX", (M, K)),
+        _ptr(dyq, _E4M3, "dyq"), _ptr(sdy, torch.float32, "sdy", (_blocks(N), M)), _ptr(wqt, _E4M3, "wqt"),
+        _ptr(sw, torch.float32, "sw", (_blocks(N), _blocks(K))), M, N, K, *_float(dX, "dX", (M, K)),
         _opt(err_word, "err_word"), _here(dyq)), "bitlinear_fp8_backward_input")
 
 
@@ -473,8 +487,8 @@ def bitlinear_fp8_backward_input(dyq, sdy, wqt, sw, dX, err_word=None):
 def bitlinear_fp8_backward_weight(dyqt, sdyt, xqt, sxt, dW, err_word=None):
     N, K, M = _codes_of(dyqt, xqt, ("dyqt", "xqt"))
     _check(lib().bitlinear_fp8_backward_weight(
-        _dev(dyqt, _E4M3, "dyqt"), _dev(sdyt, torch.float32, "sdyt", (_blocks(M), N)), _dev(xqt, _E4M3, "xqt"),
-        _dev(sxt, torch.float32, "sxt", (_blocks(M), K)), M, N, K, *_float(dW, "dW", (N, K)),
+        _ptr(dyqt, _E4M3, "dyqt"), _ptr(sdyt, torch.float32, "sdyt", (_blocks(M), N)), _ptr(xqt, _E4M3, "xqt"),
+        _ptr(sxt, torch.float32, "sxt", (_blocks(M), K)), M, N, K, *_float(dW, "dW", (N, K)),
         _opt(err_word, "err_word"), _here(dyqt)), "bitlinear_fp8_backward_weight")
 
 
