@@ -283,10 +283,13 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_forward_kernel(const TX*
             float v[kE];
             values(r, c, v);
 #pragma unroll
-            for (int e = 0; e < kE; ++e) {
-                const float z = !EDGE || k.has(e) ? v[e] - mu[r] : 0.0f;
-                q[r] = fmaf(z, z, q[r]);
-            }
+            for (int e = 0; e < kE; ++e) v[e] -= mu[r];
+            if (EDGE && !k.all())
+#pragma unroll
+                for (int e = 0; e < kE; ++e)
+                    if (!k.has(e)) v[e] = 0.0f;
+#pragma unroll
+            for (int e = 0; e < kE; ++e) q[r] = fmaf(v[e], v[e], q[r]);
         }
     }
     const float2 both = row_sum(q[0], R > 1 ? q[R - 1] : 0.0f);
@@ -518,6 +521,15 @@ __device__ __forceinline__ void fill_ring(const Place& pl, const Shape& s, const
         int64_t begin, end;
         pl.span(s, m, begin, end);
         const uint32_t n = static_cast<uint32_t>(end - begin);
+        if (s.M * s.K - end < kE) {
+            // the matrix ends inside a chunk, which no bulk copy may read as a whole: its
+            // elements come one by one (and are visible to who waits for the barrier)
+            uint8_t* raw = pl.ring + stage * (s.slot_x + s.slot_d);
+            for (int64_t i = end; i < s.M * s.K; ++i) {
+                reinterpret_cast<TX*>(raw)[i - begin] = X[i];
+                reinterpret_cast<TD*>(raw + s.slot_x)[i - begin] = dY[i];
+            }
+        }
         mbar_arrive_expect_tx(bar, n * static_cast<uint32_t>(sizeof(TX) + sizeof(TD)));
         if (n > 0) {
             bulk_load(slot, X + begin, n * static_cast<uint32_t>(sizeof(TX)), bar);
@@ -552,7 +564,6 @@ __global__ void __launch_bounds__(CH == 1 ? 800 : 640)
     Place pl(smem, s);
     const int t = pl.t, tpr = pl.tpr;
     // this thread's columns: element 0 of chunk c is column k0 + (c tpr + t) 8 - skip
-    const int64_t total = s.M * s.K;
     const int skip = EDGE ? static_cast<int>(((pl.first + pl.group) * s.K + pl.k0) & (kE - 1)) : 0;
     Mask mask[CH];
 #pragma unroll
@@ -586,7 +597,9 @@ __global__ void __launch_bounds__(CH == 1 ? 800 : 640)
         int stage = 0;
         uint32_t phase = 0;
         for (int64_t m = pl.first + pl.group; m - pl.group < s.M; m += pl.step, flat += flat_step) {
-            if (!mbar_wait_bounded(smem_u32(&pl.ctl->full[stage]), phase, &pl.ctl->abort)) break;
+            // a wait that gives up does not end the loop (the group's barriers would no longer match):
+            // the rest runs on what is there, and the block reports it at the end
+            mbar_wait_bounded(smem_u32(&pl.ctl->full[stage]), phase, &pl.ctl->abort);
             const bool live = m < s.M;
             const uint8_t* slot = pl.ring + stage * (s.slot_x + s.slot_d);
             Raw<TX> x[CH];
@@ -594,7 +607,7 @@ __global__ void __launch_bounds__(CH == 1 ? 800 : 640)
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
                 const int i = at + c * tpr * kE;
-                if (live && mask[c].any() && (!EDGE || flat + (c * tpr + 1) * kE <= total)) {
+                if (live && mask[c].any()) {
                     x[c].load(reinterpret_cast<const TX*>(slot) + i);
                     d[c].load(reinterpret_cast<const TD*>(slot + s.slot_x) + i);
                 } else {
@@ -613,16 +626,10 @@ __global__ void __launch_bounds__(CH == 1 ? 800 : 640)
             auto convert = [&](int c, float(&xv)[kE], float(&dv)[kE]) {
 #pragma unroll
                 for (int e = 0; e < kE; ++e) xv[e] = x[c][e], dv[e] = d[c][e];
-                if constexpr (EDGE) {
-                    if (mask[c].any() && flat + (c * tpr + 1) * kE > total) {
-                        load_flat(X, flat + c * tpr * kE, total, xv);  // the matrix's last chunk
-                        load_flat(dY, flat + c * tpr * kE, total, dv);
-                    }
-                    if (!mask[c].all())
+                if (EDGE && !mask[c].all())
 #pragma unroll
-                        for (int e = 0; e < kE; ++e)
-                            if (!mask[c].has(e)) xv[e] = dv[e] = 0.0f;
-                }
+                    for (int e = 0; e < kE; ++e)
+                        if (!mask[c].has(e)) xv[e] = dv[e] = 0.0f;
             };
             float xs[kOnce ? CH : 1][kE], ds[kOnce ? CH : 1][kE];
             if constexpr (kOnce)
@@ -660,10 +667,15 @@ __global__ void __launch_bounds__(CH == 1 ? 800 : 640)
                 float xv[kE], dv[kE];
                 values(c, xv, dv);
 #pragma unroll
+                for (int e = 0; e < kE; ++e) xv[e] -= mu;
+                if (EDGE && !mask[c].all())
+#pragma unroll
+                    for (int e = 0; e < kE; ++e)
+                        if (!mask[c].has(e)) xv[e] = 0.0f;
+#pragma unroll
                 for (int e = 0; e < kE; ++e) {
-                    const float z = !EDGE || mask[c].has(e) ? xv[e] - mu : 0.0f;
-                    v = fmaf(z, z, v);
-                    gx = fmaf(dv[e] * w[c][e], z, gx);
+                    v = fmaf(xv[e], xv[e], v);
+                    gx = fmaf(dv[e] * w[c][e], xv[e], gx);
                 }
             }
             const float2 both = row_sum(v, gx);
