@@ -85,6 +85,7 @@ struct Raw4<float> {
             if (k + 3 < K) a.w = __ldg(row + k + 3);
         }
     }
+    __device__ __forceinline__ float value(int j) const { return j == 0 ? a.x : j == 1 ? a.y : j == 2 ? a.z : a.w; }
     __device__ __forceinline__ void values(float (&v)[4]) const { v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w; }
 };
 template <>
@@ -103,9 +104,12 @@ struct Raw4<__nv_bfloat16> {
             for (int i = 0; i < 4; ++i) h[i] = k + i < K ? __ldg(p + i) : uint16_t(0);
         }
     }
+    __device__ __forceinline__ float value(int j) const {
+        return __uint_as_float(static_cast<uint32_t>(h[j]) << 16);
+    }
     __device__ __forceinline__ void values(float (&v)[4]) const {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(static_cast<uint32_t>(h[i]) << 16);
+        for (int i = 0; i < 4; ++i) v[i] = value(i);
     }
 };
 
@@ -186,8 +190,10 @@ struct TileArgs {
     float* st;     // columns: [groups of M, K]
 };
 
+// Three resident blocks for bf16 (8192 x 8192 weights in both orientations: 59.5 -> 55.0 us with
+// them); the fp32 values take too many registers for that.
 template <typename T, bool VEC, bool BLOCKS>
-__global__ void __launch_bounds__(32 * kTileWarps)
+__global__ void __launch_bounds__(32 * kTileWarps, sizeof(T) == 2 ? 3 : 2)
     fp8_quant_tile_kernel(const T* __restrict__ X, const TileArgs a) {
     __shared__ float colmax[kTileWarps][kG];
     __shared__ float blockmax[kTileWarps];
@@ -203,14 +209,15 @@ __global__ void __launch_bounds__(32 * kTileWarps)
     Raw4<T> x[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i].template load<VEC>(x0 + i * a.K, 4 * lane, i < rows ? cols : 0);
-    float v[8][4];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i].values(v[i]);
     Scale sc[4];  // of this thread's columns (or of the block, four times)
     if constexpr (BLOCKS) {
         float mx = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) mx = max_nan(mx, absmax4(v[i]));
+        for (int i = 0; i < 8; ++i) {
+            float v[4];
+            x[i].values(v);
+            mx = max_nan(mx, absmax4(v));
+        }
         mx = warp_absmax(mx);
         if (lane == 0) blockmax[warp] = mx;
         __syncthreads();
@@ -221,9 +228,12 @@ __global__ void __launch_bounds__(32 * kTileWarps)
     } else if (a.qt != nullptr) {
         float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < 8; ++i) {
+            float v[4];
+            x[i].values(v);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) c[j] = max_nan(c[j], fabsf(v[i][j]));
+            for (int j = 0; j < 4; ++j) c[j] = max_nan(c[j], fabsf(v[j]));
+        }
         *reinterpret_cast<float4*>(&colmax[warp][4 * lane]) = make_float4(c[0], c[1], c[2], c[3]);
         __syncthreads();
         if (threadIdx.x < kG) {
@@ -245,7 +255,9 @@ __global__ void __launch_bounds__(32 * kTileWarps)
             float absmax = 0.0f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float m = warp_absmax(absmax4(v[i]));
+                float v[4];
+                x[i].values(v);
+                const float m = warp_absmax(absmax4(v));
                 if (lane == i) absmax = m;
             }
             mine = scale_of(absmax, a.eps);
@@ -255,14 +267,17 @@ __global__ void __launch_bounds__(32 * kTileWarps)
         for (int i = 0; i < 8; ++i) {
             const float ratio = BLOCKS ? mine.ratio : __shfl_sync(0xFFFFFFFFu, mine.ratio, i);
             // the last group's codes are padded with zeros to the pitch
+            float v[4];
+            x[i].values(v);
             if (i < rows && k0 < a.pitch)
-                *reinterpret_cast<uint32_t*>(a.q + (m0 + i) * a.pitch + k0) = keep(codes4(v[i], ratio), cols - 4 * lane);
+                *reinterpret_cast<uint32_t*>(a.q + (m0 + i) * a.pitch + k0) = keep(codes4(v, ratio), cols - 4 * lane);
         }
     }
     if (a.qt == nullptr) return;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const float lo[4] = {v[0][j], v[1][j], v[2][j], v[3][j]}, hi[4] = {v[4][j], v[5][j], v[6][j], v[7][j]};
+        const float lo[4] = {x[0].value(j), x[1].value(j), x[2].value(j), x[3].value(j)};
+        const float hi[4] = {x[4].value(j), x[5].value(j), x[6].value(j), x[7].value(j)};
         *reinterpret_cast<uint2*>(turn + (4 * lane + j) * kG + 8 * (warp ^ (lane & 15))) =
             make_uint2(keep(codes4(lo, sc[j].ratio), rows), keep(codes4(hi, sc[j].ratio), rows - 4));
     }
