@@ -395,7 +395,7 @@ BL_API bl_status bitlinear_ste_backward_weight(const float *dY, const int8_t *xq
  * order fixed by the shape, so results repeat bit for bit.
  * Types: x_dtype, y_dtype, dy_dtype, dx_dtype are each BL_OUT_F32 or BL_OUT_BF16.  Any
  * K >= 1; M, K <= 2^30, M * K <= 2^40.  Rows are contiguous ([M, K] row-major); K % 8 == 0
- * runs with 16-byte accesses.  Outputs must not overlap inputs or each other.
+ * is the fastest.  Outputs must not overlap inputs or each other.
  * ---------------------------------------------------------------------------------- */
 
 /*   X           in  : [M, K] of x_dtype, device.

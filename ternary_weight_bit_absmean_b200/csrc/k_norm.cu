@@ -112,9 +112,8 @@ struct Mask {
     __device__ __forceinline__ bool has(int e) const { return e >= lo && e < hi; }
 };
 
-// A chunk of the matrix at flat element `flat` (a multiple of eight) from global memory: one
-// access if it lies inside the matrix of `total` elements, else element by element (only the
-// matrix's last chunk).
+// The chunk at flat element `flat` (a multiple of eight) of a matrix of `total` elements, element by
+// element: only for the matrix's last chunk, which may end inside.
 template <typename T>
 __device__ __forceinline__ void load_flat(const T* base, int64_t flat, int64_t total, float (&v)[kE]) {
 #pragma unroll

@@ -215,6 +215,24 @@ def test_products(M, N, K):
     check_products(M, N, K, seed=M)
 
 
+# One shape for every form the products choose between: token tiles of 16 to 128 with and without a
+# split of the contraction, tiles of 256 x 128 and 256 x 256, one round of tiles and several.
+@pytest.mark.parametrize("M,N,K", [
+    (5, 28700, 1000), (16, 1024, 8192), (30, 129, 2048), (60, 3000, 1100), (100, 1024, 4099), (130, 8192, 300),
+    (512, 4096, 1536), (1000, 9000, 256), (2304, 5000, 400), (257, 19000, 129)])
+def test_every_form_of_the_products(M, N, K):
+    check_products(M, N, K, seed=N)
+
+
+def test_tall_and_flat_weight_gradients():
+    """dW = dY^T x with few outputs and many tokens, and the reverse."""
+    for M, N, K in [(20000, 130, 70), (3, 2100, 1800), (129, 4000, 260)]:
+        x, _, dy = problem(M, N, K, 3)
+        _, _, xt, sxt = B.fp8_quantize_act(x, transposed=True)
+        _, _, dt, sdt = B.fp8_quantize_act(dy, 1e-12, transposed=True)
+        close(B.fp8_backward_weight(dt, sdt, xt, sxt), rows_of(dt, sdt, M), rows_of(xt, sxt, M), (M, N, K))
+
+
 def test_group_sums_keep_fp32_digits():
     """Large products that cancel within a group next to small ones: what the accumulation
     keeps of the small ones is bounded by the fp32 rounding of the large ones' magnitude."""

@@ -229,6 +229,40 @@ def test_captured_and_replayed_on_new_inputs():
     assert all(torch.equal(p, q) for p, q in zip((dx, dw, db), B.norm_backward(dy2, x2, w, bias=True)))
 
 
+@pytest.mark.parametrize("M,K", [(40, 100), (700, 515), (100, 9000), (60, 20000)])
+def test_one_call_does_not_read_what_another_left(M, K):
+    """Back to back on the same workspace and outputs: each call's sums are its own."""
+    a, w, _, da = inputs(M, K, seed=21)
+    b, _, _, db = inputs(M, K, seed=22)
+    n = max(1, B.bitlinear_norm_backward_workspace_size(M, K))
+    ws = torch.empty(n, dtype=torch.uint8, device=DEV)
+    out = [torch.empty(M, K, device=DEV), torch.empty(K, device=DEV), torch.empty(K, device=DEV)]
+    for x, dy in ((a, da), (b, db), (a, da)):
+        B.bitlinear_norm_backward(dy, x, w, LAYER, 1e-5, *out, ws)
+        assert all(torch.equal(p, q) for p, q in zip(out, B.norm_backward(dy, x, w, LAYER, bias=True)))
+
+
+def test_two_graphs_with_workspaces_of_their_own():
+    x, w, _, dy = inputs(500, 1536, seed=23)
+    x2, _, _, dy2 = inputs(500, 1536, seed=24)
+    want, want2 = B.norm_backward(dy, x, w, bias=True), B.norm_backward(dy2, x2, w, bias=True)
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for a, d in ((x, dy), (x2, dy2)):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(B.norm_backward(d, a, w, bias=True))
+        graphs.append(g)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(20):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(outs[0], want))
+    assert all(torch.equal(p, q) for p, q in zip(outs[1], want2))
+
+
 def test_offsets_past_32_bits():
     M, K = 70001, 32768                                 # 2.3e9 elements
     x = torch.empty(M, K, dtype=BF16, device=DEV)
