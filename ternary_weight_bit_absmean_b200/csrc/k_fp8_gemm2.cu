@@ -46,7 +46,7 @@ constexpr int kG = 128;
 constexpr int kThreads = 384;
 constexpr int kWarpTma = 0, kWarpMma = 1, kWarpScale = 2, kWarpEpi = 4, kEpiWarps = 8;
 constexpr int kSlots = 8;             // scale ring
-constexpr int kTurnBytes = 2048;      // of an epilogue warp: 32 rows x 64 bytes of output
+constexpr int kTurnBytes = 4096;      // of an epilogue warp: 32 rows x 128 bytes of output
 
 // TP: columns of a tile (rows of Pm), 256 or 128.
 template <int TP>
@@ -106,19 +106,19 @@ __device__ __forceinline__ void add_scaled2(const uint32_t* v, uint64_t scale, f
 
 // The sums of a warp's 32 rows (one per lane) x kCols columns -> out.
 // A row's sums sit in one thread, so storing them from there would write 32 scattered pieces
-// per instruction; they are turned in shared memory (64 bytes of every row at a time, 16-byte
-// chunks swizzled so that neither side has bank conflicts) and leave as runs of 64 bytes.
+// per instruction; they are turned in shared memory (128 bytes of every row at a time, 16-byte
+// chunks swizzled so that neither side has bank conflicts) and leave as whole 128-byte lines.
 template <typename T, int kCols>
 __device__ __forceinline__ void store_rows(const Fp8Product& d, int64_t q, int64_t p, const float (&acc)[kCols],
                                            uint8_t* turn, int lane) {
-    constexpr int kPer = 64 / static_cast<int>(sizeof(T));  // columns per round: 16 or 32
+    constexpr int kPer = 128 / static_cast<int>(sizeof(T));  // columns per round: 32 or 64
     const bool wide = (d.P * static_cast<int64_t>(sizeof(T))) % 16 == 0;
     T* out = static_cast<T*>(d.out);
 #pragma unroll
     for (int c0 = 0; c0 < kCols; c0 += kPer) {
         __syncwarp();
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < 8; ++c) {
             uint4 w;
             if constexpr (sizeof(T) == 2) {
                 const float* s = &acc[c0 + 8 * c];
@@ -129,23 +129,25 @@ __device__ __forceinline__ void store_rows(const Fp8Product& d, int64_t q, int64
                 w = make_uint4(__float_as_uint(s[0]), __float_as_uint(s[1]), __float_as_uint(s[2]),
                                __float_as_uint(s[3]));
             }
-            *reinterpret_cast<uint4*>(turn + 64 * lane + ((c ^ ((lane >> 1) & 3)) << 4)) = w;
+            *reinterpret_cast<uint4*>(turn + 128 * lane + ((c ^ (lane & 7)) << 4)) = w;
         }
         __syncwarp();
         if (wide) {
-            const int64_t pc = p + c0 + (lane & 3) * (16 / static_cast<int>(sizeof(T)));
+            const int64_t pc = p + c0 + (lane & 7) * (16 / static_cast<int>(sizeof(T)));
+            const int64_t left = pc < d.P ? d.Q - q : 0;  // rows to store
+            T* o = out + q * d.P + pc;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = 8 * i + (lane >> 2);
-                const uint4 w = *reinterpret_cast<const uint4*>(turn + 64 * r + (((lane & 3) ^ ((r >> 1) & 3)) << 4));
-                if (q + r < d.Q && pc < d.P) *reinterpret_cast<uint4*>(out + (q + r) * d.P + pc) = w;
+            for (int i = 0; i < 8; ++i) {
+                const int r = 4 * i + (lane >> 3);
+                const uint4 w = *reinterpret_cast<const uint4*>(turn + 128 * r + (((lane & 7) ^ (r & 7)) << 4));
+                if (r < left) *reinterpret_cast<uint4*>(o + r * d.P) = w;
             }
         } else {
             // rows of `out` start anywhere: neighbouring lanes store neighbouring elements
             for (int e = lane; e < 32 * kPer; e += 32) {
                 const int r = e / kPer, c = e % kPer;
                 const int byte = c * static_cast<int>(sizeof(T));
-                const T v = *reinterpret_cast<const T*>(turn + 64 * r + (((byte >> 4) ^ ((r >> 1) & 3)) << 4) + (byte & 15));
+                const T v = *reinterpret_cast<const T*>(turn + 128 * r + (((byte >> 4) ^ (r & 7)) << 4) + (byte & 15));
                 if (q + r < d.Q && p + c0 + c < d.P) out[(q + r) * d.P + p + c0 + c] = v;
             }
         }
