@@ -143,12 +143,25 @@ __device__ __forceinline__ void store_rows(const Fp8Product& d, int64_t q, int64
                 if (r < left) *reinterpret_cast<uint4*>(o + r * d.P) = w;
             }
         } else {
-            // rows of `out` start anywhere: neighbouring lanes store neighbouring elements
-            for (int e = lane; e < 32 * kPer; e += 32) {
-                const int r = e / kPer, c = e % kPer;
-                const int byte = c * static_cast<int>(sizeof(T));
-                const T v = *reinterpret_cast<const T*>(turn + 128 * r + (((byte >> 4) ^ (r & 7)) << 4) + (byte & 15));
-                if (q + r < d.Q && p + c0 + c < d.P) out[(q + r) * d.P + p + c0 + c] = v;
+            // rows of `out` start anywhere: a lane stores four bytes of a row, in one piece where
+            // they are aligned
+            constexpr int kPair = 4 / static_cast<int>(sizeof(T));
+            const int64_t pc = p + c0 + lane * kPair, room = d.P - pc;
+            const int n = d.Q - q < 32 ? static_cast<int>(d.Q - q) : 32;
+            T* o = out + q * d.P + pc;
+            if (room > 0) {
+#pragma unroll 4
+                for (int r = 0; r < n; ++r, o += d.P) {
+                    const uint32_t w =
+                        *reinterpret_cast<const uint32_t*>(turn + 128 * r + (((lane >> 2) ^ (r & 7)) << 4) + 4 * (lane & 3));
+                    if (room >= kPair && (reinterpret_cast<uintptr_t>(o) & 3u) == 0) {
+                        *reinterpret_cast<uint32_t*>(o) = w;
+                    } else {
+                        uint16_t* h = reinterpret_cast<uint16_t*>(o);  // only bf16 comes here
+                        h[0] = static_cast<uint16_t>(w);
+                        if (room > 1) h[1] = static_cast<uint16_t>(w >> 16);
+                    }
+                }
             }
         }
     }
