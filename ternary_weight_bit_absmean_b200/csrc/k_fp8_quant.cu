@@ -65,17 +65,20 @@ __device__ __forceinline__ uint32_t keep(uint32_t codes, int n) {
 
 // Elements k .. k+3 of a row of K as they lie in memory, zeros past its end (all bits zero is a
 // zero in either type).  Loading and converting are apart so that a thread's loads are all on
-// their way before the first is needed.  VEC: K % 4 == 0 (k is), so the four are there or not
-// together and lie on their own alignment.
-template <typename T>
+// their way before the first is needed: load() of every group, then settle() of every group,
+// then the values.  VEC: K % 4 == 0 (k is), so the four are there or not together and lie on
+// their own alignment.  In other rows four fp32 loads of neighbouring lanes still fill whole
+// lines (8191 x 4099: 28 us, 92 % of the copy rate).  In bf16 there are twice as many loads to a
+// byte: there the two aligned groups of four around the four are loaded and the four cut out of
+// them (tiles of 4095 x 4099 both ways 33 -> 25 us, weights 28.5 -> 21, rows of 8191 x 4099
+// 33 -> 31).
+template <typename T, bool VEC>
 struct Raw4;
-template <>
-struct Raw4<float> {
+template <bool VEC>
+struct Raw4<float, VEC> {
     float4 a;
-    __device__ __forceinline__ void clear() { a = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
-    template <bool VEC>
-    __device__ __forceinline__ void load(const float* row, int k, int K) {
-        clear();
+    __device__ __forceinline__ void load(const float* row, int k, int K, const float*) {
+        a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if constexpr (VEC) {
             if (k < K) a = __ldg(reinterpret_cast<const float4*>(row + k));
         } else {
@@ -85,27 +88,60 @@ struct Raw4<float> {
             if (k + 3 < K) a.w = __ldg(row + k + 3);
         }
     }
+    __device__ __forceinline__ void settle(const float*, int, int) {}
     __device__ __forceinline__ float value(int j) const { return j == 0 ? a.x : j == 1 ? a.y : j == 2 ? a.z : a.w; }
     __device__ __forceinline__ void values(float (&v)[4]) const { v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w; }
 };
 template <>
-struct Raw4<__nv_bfloat16> {
+struct Raw4<__nv_bfloat16, true> {
     uint16_t h[4];
-    __device__ __forceinline__ void clear() { h[0] = h[1] = h[2] = h[3] = 0; }
-    template <bool VEC>
-    __device__ __forceinline__ void load(const __nv_bfloat16* row, int k, int K) {
+    __device__ __forceinline__ void load(const __nv_bfloat16* row, int k, int K, const __nv_bfloat16*) {
         const uint16_t* p = reinterpret_cast<const uint16_t*>(row + k);
-        if constexpr (VEC) {
-            uint2 a = make_uint2(0u, 0u);
-            if (k < K) a = __ldg(reinterpret_cast<const uint2*>(p));
-            *reinterpret_cast<uint2*>(h) = a;
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) h[i] = k + i < K ? __ldg(p + i) : uint16_t(0);
-        }
+        uint2 a = make_uint2(0u, 0u);
+        if (k < K) a = __ldg(reinterpret_cast<const uint2*>(p));
+        *reinterpret_cast<uint2*>(h) = a;
     }
+    __device__ __forceinline__ void settle(const __nv_bfloat16*, int, int) {}
     __device__ __forceinline__ float value(int j) const {
         return __uint_as_float(static_cast<uint32_t>(h[j]) << 16);
+    }
+    __device__ __forceinline__ void values(float (&v)[4]) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = value(i);
+    }
+};
+template <>
+struct Raw4<__nv_bfloat16, false> {
+    uint2 a, b;  // b: the group behind a's, until settle()
+    __device__ __forceinline__ static int offset(const __nv_bfloat16* p) {
+        return static_cast<int>(reinterpret_cast<uintptr_t>(p) >> 1) & 3;
+    }
+    // `end` is the end of the matrix, which may lie inside an aligned group
+    __device__ __forceinline__ void load(const __nv_bfloat16* row, int k, int K, const __nv_bfloat16* end) {
+        a = b = make_uint2(0u, 0u);
+        if (k >= K) return;
+        const uint16_t* at = reinterpret_cast<const uint16_t*>(row + k) - offset(row + k);
+        if (at + 8 <= reinterpret_cast<const uint16_t*>(end)) {
+            a = __ldg(reinterpret_cast<const uint2*>(at));
+            b = __ldg(reinterpret_cast<const uint2*>(at) + 1);
+        } else {
+            const int there = static_cast<int>(reinterpret_cast<const uint16_t*>(end) - at);
+            auto get = [&](int i) { return i < there ? static_cast<uint32_t>(__ldg(at + i)) << (16 * (i & 1)) : 0u; };
+            a = make_uint2(get(0) | get(1), get(2) | get(3));
+            b = make_uint2(get(4) | get(5), get(6) | get(7));
+        }
+    }
+    __device__ __forceinline__ void settle(const __nv_bfloat16* row, int k, int K) {
+        const int off = offset(row + k), n = K - k;
+        uint32_t third = b.x;
+        if (off & 2) a = make_uint2(a.y, b.x), third = b.y;
+        if (off & 1) a = make_uint2(__funnelshift_r(a.x, a.y, 16), __funnelshift_r(a.y, third, 16));
+        if (n < 4) a.y &= n < 3 ? 0u : 0xFFFFu;
+        if (n < 2) a.x &= n < 1 ? 0u : 0xFFFFu;
+    }
+    __device__ __forceinline__ float value(int j) const {
+        const uint32_t w = j < 2 ? a.x : a.y;
+        return __uint_as_float((j & 1) ? (w & 0xFFFF0000u) : (w << 16));
     }
     __device__ __forceinline__ void values(float (&v)[4]) const {
 #pragma unroll
@@ -126,7 +162,7 @@ constexpr int kU = 8;
 constexpr int kRowWarps = 8;
 
 template <typename T, bool VEC, int LG>
-__global__ void __launch_bounds__(32 * kRowWarps, 5)
+__global__ void __launch_bounds__(32 * kRowWarps, sizeof(T) == 4 || VEC ? 5 : 4)
     fp8_quant_rows_kernel(const T* __restrict__ X, int64_t M, int64_t K, int64_t pitch, float eps,
                           uint8_t* __restrict__ q, float* __restrict__ s, uint32_t spans) {
     pdl_wait_then_release();
@@ -142,10 +178,13 @@ __global__ void __launch_bounds__(32 * kRowWarps, 5)
     const int64_t rest = K - g0 * kG;
     const int n = rest < 2 * kAcross * kG ? static_cast<int>(rest) : 2 * kAcross * kG;
     const T* x0 = X + m0 * K + g0 * kG;
-    Raw4<T> x[kU];
+    Raw4<T, VEC> x[kU];
 #pragma unroll
     for (int u = 0; u < kU; ++u)
-        x[u].template load<VEC>(x0 + (u / kAcross) * K, u % kAcross * kG + 4 * lane, u / kAcross < rows ? n : 0);
+        x[u].load(x0 + (u / kAcross) * K, u % kAcross * kG + 4 * lane, u / kAcross < rows ? n : 0, X + M * K);
+#pragma unroll
+    for (int u = 0; u < kU; ++u)
+        x[u].settle(x0 + (u / kAcross) * K, u % kAcross * kG + 4 * lane, u / kAcross < rows ? n : 0);
     float absmax = 0.0f;
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
@@ -193,7 +232,7 @@ struct TileArgs {
 // Three resident blocks for bf16 (8192 x 8192 weights in both orientations: 59.5 -> 55.0 us with
 // them); the fp32 values take too many registers for that.
 template <typename T, bool VEC, bool BLOCKS>
-__global__ void __launch_bounds__(32 * kTileWarps, sizeof(T) == 2 ? 3 : 2)
+__global__ void __launch_bounds__(32 * kTileWarps, sizeof(T) == 2 && VEC ? 3 : 2)
     fp8_quant_tile_kernel(const T* __restrict__ X, const TileArgs a) {
     __shared__ float colmax[kTileWarps][kG];
     __shared__ float blockmax[kTileWarps];
@@ -206,9 +245,11 @@ __global__ void __launch_bounds__(32 * kTileWarps, sizeof(T) == 2 ? 3 : 2)
     const int rows = a.M - m0 < 8 ? static_cast<int>(a.M - m0) : 8;
     const int cols = a.K - tk * kG < kG ? static_cast<int>(a.K - tk * kG) : kG;
     const T* x0 = X + m0 * a.K + tk * kG;
-    Raw4<T> x[8];
+    Raw4<T, VEC> x[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i].template load<VEC>(x0 + i * a.K, 4 * lane, i < rows ? cols : 0);
+    for (int i = 0; i < 8; ++i) x[i].load(x0 + i * a.K, 4 * lane, i < rows ? cols : 0, X + a.M * a.K);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i].settle(x0 + i * a.K, 4 * lane, i < rows ? cols : 0);
     Scale sc[4];  // of this thread's columns (or of the block, four times)
     if constexpr (BLOCKS) {
         float mx = 0.0f;
