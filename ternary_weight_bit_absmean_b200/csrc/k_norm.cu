@@ -184,28 +184,53 @@ __device__ __forceinline__ void load_vector(const float* p, float fill, int64_t 
     for (int e = 0; e < kE; ++e) v[e] = p != nullptr && m.has(e) ? __ldg(p + k + e) : fill;
 }
 
-// Sums of two values over the threads of a group.  Slots alternate between calls: one is
-// written again only after a barrier that every reader of it has passed.
+// Sums of two values over the threads of a group.  Slots alternate between calls: one is written
+// again only after a barrier that every reader of it has passed.  HALVES: each half of a warp adds
+// one of the two, which takes half the exchanges and some registers (backward of 8192 x 3200 layer
+// bf16 84 -> 77 us; in the widest blocks, whose registers are short, 142 -> 164 for 8192 x 8640 RMS
+// fp32, so these add both in every lane).
+template <bool HALVES>
 struct GroupSum {
     float2* buf;  // [2][32] of this group
     int t, tpr, group;
     uint32_t calls = 0;
     __device__ __forceinline__ float2 operator()(float a, float b) {
+        if constexpr (HALVES) {
+            const bool upper = (t & 16) != 0;
+            float v = upper ? b : a;
+            v += __shfl_xor_sync(0xFFFFFFFFu, upper ? a : b, 16);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
-            b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
-        }
-        if (tpr > 32) {
-            float2* s = buf + 32 * (calls & 1);
-            if ((t & 31) == 0) s[t >> 5] = make_float2(a, b);
-            asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(tpr) : "memory");
-            const float2 v = (t & 31) < (tpr >> 5) ? s[t & 31] : make_float2(0.0f, 0.0f);
-            a = v.x, b = v.y;
+            for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+            if (tpr > 32) {
+                // the warps' sums of a, then those of b
+                float* s = reinterpret_cast<float*>(buf + 32 * (calls & 1)) + 2 * (t & 16);
+                const int i = t & 15, n = tpr >> 5;
+                if (i == 0) s[t >> 5] = v;
+                asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(tpr) : "memory");
+                v = i < n ? s[i] : 0.0f;
+                if (i + 16 < n) v += s[i + 16];
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+            }
+            a = __shfl_sync(0xFFFFFFFFu, v, 0);
+            b = __shfl_sync(0xFFFFFFFFu, v, 16);
+        } else {
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) {
                 a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
                 b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
+            }
+            if (tpr > 32) {
+                float2* s = buf + 32 * (calls & 1);
+                if ((t & 31) == 0) s[t >> 5] = make_float2(a, b);
+                asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(tpr) : "memory");
+                const float2 v = (t & 31) < (tpr >> 5) ? s[t & 31] : make_float2(0.0f, 0.0f);
+                a = v.x, b = v.y;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) {
+                    a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+                    b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
+                }
             }
         }
         ++calls;
@@ -233,7 +258,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_forward_kernel(const TX*
     __shared__ float2 sums[8][64];
     const int t = threadIdx.x, tpr = blockDim.x, group = threadIdx.y;
     pdl_wait_then_release();
-    GroupSum row_sum{sums[group], t, tpr, group};
+    GroupSum<true> row_sum{sums[group], t, tpr, group};
     const int64_t m0 = (static_cast<int64_t>(blockIdx.x) * blockDim.y + group) * R;
     if (m0 >= a.M) return;  // a whole group leaves together
     const int64_t total = a.M * a.K;
@@ -427,8 +452,9 @@ struct Control {
 
 // GroupSum, then over the blocks of the cluster (each sends its sums to all).  A slot is
 // written again only after the other blocks' next sums, sent by threads that have read it.
+template <bool HALVES>
 struct RowSum {
-    GroupSum local;
+    GroupSum<HALVES> local;
     Control* ctl;
     int cluster;
     uint32_t rank;
@@ -579,10 +605,11 @@ struct BwdArgs {
 };
 
 // DB: with the bias's gradient (its sums take registers).
-template <typename TX, typename TD, bool EDGE, bool DB, int CH>
-__global__ void __launch_bounds__(CH == 1 ? 800 : 640)
+template <typename TX, typename TD, bool EDGE, bool DB, int CH, int THREADS>
+__global__ void __launch_bounds__(THREADS)
     norm_backward_kernel(const TX* __restrict__ X, const TD* __restrict__ dY, const __grid_constant__ BwdArgs a) {
     extern __shared__ __align__(128) uint8_t smem[];
+    constexpr bool kHalves = THREADS < 640 || CH == 1;
     const Shape& s = a.s;
     Place pl(smem, s);
     const int t = pl.t, tpr = pl.tpr;
@@ -605,7 +632,8 @@ __global__ void __launch_bounds__(CH == 1 ? 800 : 640)
     if (pl.producer) {
         fill_ring<TX, TD>(pl, s, X, dY);
     } else {
-        RowSum row_sum{GroupSum{pl.ctl->sums[pl.group], t, tpr, pl.group}, pl.ctl, pl.cluster, pl.rank};
+        RowSum<kHalves> row_sum{GroupSum<kHalves>{pl.ctl->sums[pl.group], t, tpr, pl.group}, pl.ctl, pl.cluster,
+                                pl.rank};
         float w[CH][kE];
 #pragma unroll
         for (int c = 0; c < CH; ++c) load_vector<EDGE>(a.w, 1.0f, pl.k0 + (c * tpr + t) * kE - skip, s.K, mask[c], w[c]);
@@ -910,9 +938,19 @@ cudaError_t forward_x(const TX* X, const FwdArgs& a, cudaStream_t stream) {
     return a.K % kE == 0 ? forward_t<TX, false>(X, a, stream) : forward_t<TX, true>(X, a, stream);
 }
 
-// Backward: how rows of K columns are laid over blocks.  Up to 4096 columns a thread owns one
-// chunk, up to kSlice two; longer rows go to the smallest cluster whose slices fit (a power of
-// two up to eight).  Several rows share a block as long as the rows still spread over all SMs.
+// Backward: how rows of K columns are laid over blocks.  Up to kSlice columns a row is one block's;
+// longer ones go to the smallest cluster whose slices fit (a power of two up to eight).  Several
+// rows share a block as long as the rows still spread over all SMs.
+//
+// A thread owns one chunk up to 3072 columns and two or three above.  What decides is how many warps
+// the registers of its columns (x, dy, w, dw and with a bias db) leave room for: a warp too many on
+// one of the SM's four schedulers takes registers from all of them, and the sums spill.
+//   - two chunks for 3073 to 4096 columns, so that two rows fit a block: 8192 x 3200 RMS 60 -> 47 us,
+//     layer fp32 85 -> 62 (4096 layer fp32 loses, 102 -> 114).  With fewer rows than SMs one chunk is
+//     quicker (32 x 4096: 6.6 against 6.1 us).
+//   - three chunks where two would need sixteen warps beside the one that fills the ring: 8192 x 8192
+//     layer 232 -> 143 us in fp32, 131 -> 113 in bf16 (RMS loses, 121 -> 125; both must take the same
+//     so that leaving out db changes no bit of dw).
 struct Plan {
     int cluster, chunks;  // blocks of a row, chunks of a thread
     Shape s;
@@ -927,15 +965,16 @@ Plan plan_of(int64_t M, int64_t K, int ex, int ed) {
     while ((K + p.cluster - 1) / p.cluster > kSlice) p.cluster *= 2;
     const int64_t slice = ((K + p.cluster - 1) / p.cluster + kE - 1) / kE * kE;
     const int64_t chunks = chunks_of(p.cluster > 1 ? slice - (K % kE != 0) : K);  // unaligned: one more
-    p.chunks = chunks <= 513 ? 1 : 2;
+    const int64_t spread = (M + kParts - 1) / kParts;  // rows of a block when all SMs have some
+    p.chunks = chunks <= (spread > 1 ? 384 : 513) ? 1 : chunks > 960 && chunks <= 1056 ? 3 : 2;
     Shape& s = p.s;
     s.M = M;
     s.K = K;
     s.slice = static_cast<int>(p.cluster > 1 ? slice : K);
     s.tpr = static_cast<int>(((chunks + p.chunks - 1) / p.chunks + 31) / 32 * 32);
-    const int64_t spread = (M + kParts - 1) / kParts;  // rows of a block when all SMs have some
     const int fit = p.cluster > 1 ? 1 : (p.chunks == 1 ? 768 : 608) / s.tpr;
     s.groups = fit < kMaxGroups ? fit : kMaxGroups;
+    if (s.groups >= 8 && s.groups * s.tpr == 768) --s.groups;  // room for 80 registers, see below
     if (s.groups > spread) s.groups = static_cast<int>(spread);
     const int64_t batches = (M + s.groups - 1) / s.groups;
     const int most = kParts / p.cluster;
@@ -971,26 +1010,38 @@ int backward_parts(int64_t M, int64_t K) {
     return static_cast<int>(strips < kParts ? strips : kParts);
 }
 
-template <typename TX, typename TD, bool EDGE, bool DB, int CH>
+template <typename TX, typename TD, bool EDGE, bool DB, int CH, int THREADS>
 cudaError_t backward_c(const TX* X, const TD* dY, const Plan& p, const BwdArgs& a, cudaStream_t stream) {
     static PerContextOnce attr;
     cudaError_t e = attr.run([] {
-        return cudaFuncSetAttribute(norm_backward_kernel<TX, TD, EDGE, DB, CH>,
+        return cudaFuncSetAttribute(norm_backward_kernel<TX, TD, EDGE, DB, CH, THREADS>,
                                     cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost);
     });
     if (e != cudaSuccess) return e;
-    return launch_pdl(norm_backward_kernel<TX, TD, EDGE, DB, CH>, dim3(static_cast<unsigned>(p.parts * p.cluster)),
-                      dim3(p.s.tpr * p.s.groups + 32), smem_of(p), stream,
+    return launch_pdl(norm_backward_kernel<TX, TD, EDGE, DB, CH, THREADS>,
+                      dim3(static_cast<unsigned>(p.parts * p.cluster)), dim3(p.s.tpr * p.s.groups + 32), smem_of(p), stream,
                       p.cluster > 1 ? dim3(p.cluster, 1, 1) : dim3(kNoCluster), X, dY, a);
 }
 
+// The kernel whose limit of threads leaves the most registers: 80 with up to 768, 128 with up to 512,
+// 168 with up to 384 (8192 x 7680 layer fp32 at 128 registers 134 us, at the 96 of 640 threads 210).
+// Without a bias 96 do, and what more there is only lets the compiler move loads (8192 x 7680 RMS:
+// 104 against 116 us).
 template <typename TX, typename TD, bool EDGE>
 cudaError_t backward_e(const TX* X, const TD* dY, const Plan& p, const BwdArgs& a, cudaStream_t stream) {
-    if (a.db != nullptr)
-        return p.chunks == 1 ? backward_c<TX, TD, EDGE, true, 1>(X, dY, p, a, stream)
-                             : backward_c<TX, TD, EDGE, true, 2>(X, dY, p, a, stream);
-    return p.chunks == 1 ? backward_c<TX, TD, EDGE, false, 1>(X, dY, p, a, stream)
-                         : backward_c<TX, TD, EDGE, false, 2>(X, dY, p, a, stream);
+    if (a.db != nullptr) {
+        if (p.chunks == 1)
+            return p.s.tpr * p.s.groups < 768 ? backward_c<TX, TD, EDGE, true, 1, 768>(X, dY, p, a, stream)
+                                              : backward_c<TX, TD, EDGE, true, 1, 800>(X, dY, p, a, stream);
+        if (p.chunks == 3) return backward_c<TX, TD, EDGE, true, 3, 384>(X, dY, p, a, stream);
+        if (p.s.tpr * p.s.groups < 512) return backward_c<TX, TD, EDGE, true, 2, 512>(X, dY, p, a, stream);
+        return backward_c<TX, TD, EDGE, true, 2, 640>(X, dY, p, a, stream);
+    }
+    if (p.chunks == 1)
+        return p.s.tpr * p.s.groups < 768 ? backward_c<TX, TD, EDGE, false, 1, 768>(X, dY, p, a, stream)
+                                          : backward_c<TX, TD, EDGE, false, 1, 800>(X, dY, p, a, stream);
+    if (p.chunks == 3) return backward_c<TX, TD, EDGE, false, 3, 384>(X, dY, p, a, stream);
+    return backward_c<TX, TD, EDGE, false, 2, 640>(X, dY, p, a, stream);
 }
 
 struct BwdCall {

@@ -146,6 +146,16 @@ def test_backward(M, K, kind):
         close(hx, px, ptx, "dx without w")
 
 
+# One shape for every way in which rows are laid over blocks: one to three chunks a thread, one row
+# of a block or several, whole chunks or not, a block or a cluster to a row.
+@pytest.mark.parametrize("M,K", [(1200, 256), (1210, 129), (700, 1536), (310, 2051), (400, 3201), (400, 4096), (310, 4607),
+                                 (300, 4864), (200, 5121), (170, 7680), (330, 7999), (310, 8192), (300, 8447),
+                                 (170, 9001), (160, 16384), (90, 16389)])
+@pytest.mark.parametrize("kind", [RMS, LAYER])
+def test_backward_in_every_layout(M, K, kind):
+    test_backward(M, K, kind)
+
+
 @pytest.mark.parametrize("kind", [RMS, LAYER])
 def test_backward_against_differences(kind):
     """Central differences of L = sum dy y(x, w, b) in 64 bits, every input element."""
