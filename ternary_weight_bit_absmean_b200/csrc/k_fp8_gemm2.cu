@@ -19,7 +19,7 @@
 // cycles against 230, more than the tensor pipe needs for them.  The register file is split
 // by setmaxnreg.  All waits are bounded as in the ternary kernels; no load uses multicast.
 //
-// Measured (bf16 output): 8192 x 8640 x 3200 in 217 us, 2.08 PFLOP/s; with the epilogue taken
+// Measured (bf16 output): 8192 x 8640 x 3200 in 216 us, 2.10 PFLOP/s; with the epilogue taken
 // out, loads and MMAs alone run at 3.05.  What is left is the hand-over of the two
 // accumulators (an accumulator is busy for its MMAs, the commit, the readers' 430 cycles and
 // their signal back: about 1660 cycles for two groups on an idle GPU) and the clock, which
