@@ -942,10 +942,10 @@ cudaError_t forward_x(const TX* X, const FwdArgs& a, cudaStream_t stream) {
 // longer ones go to the smallest cluster whose slices fit (a power of two up to eight).  Several
 // rows share a block as long as the rows still spread over all SMs.
 //
-// A thread owns one chunk up to 3072 columns and two or three above.  What decides is how many warps
+// A thread owns one chunk in rows of up to 384 and two or three above.  What decides is how many warps
 // the registers of its columns (x, dy, w, dw and with a bias db) leave room for: a warp too many on
 // one of the SM's four schedulers takes registers from all of them, and the sums spill.
-//   - two chunks for 3073 to 4096 columns, so that two rows fit a block: 8192 x 3200 RMS 60 -> 47 us,
+//   - two chunks from there to 4096 columns, so that two rows fit a block: 8192 x 3200 RMS 60 -> 47 us,
 //     layer fp32 85 -> 62 (4096 layer fp32 loses, 102 -> 114).  With fewer rows than SMs one chunk is
 //     quicker (32 x 4096: 6.6 against 6.1 us).
 //   - three chunks where two would need sixteen warps beside the one that fills the ring: 8192 x 8192
