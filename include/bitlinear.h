@@ -391,7 +391,9 @@ BL_API bl_status bitlinear_ste_backward_weight(const float *dY, const int8_t *xq
  *   backward: g = dy * w_k;  c1 = sum_k g n / K;  c2 = 0 (RMS) or sum_k g / K (LAYER)
  *             dx = r * (g - c2 - n * c1);  dw_k = sum_m dy n;  db_k = sum_m dy
  * All arithmetic and sums are fp32, rounded once to the output type; infinities and NaN
- * spread to their row (and to the column sums) as the formulas say.  The sums run in an
+ * spread to their row (and to the column sums) as the formulas say.  The mean is taken from
+ * differences between the row's elements and kept in two fp32 parts, so a mean far above
+ * the spread costs n no digits, and a constant row gives n = 0.  The sums run in an
  * order fixed by the shape, so results repeat bit for bit.
  * Types: x_dtype, y_dtype, dy_dtype, dx_dtype are each BL_OUT_F32 or BL_OUT_BF16.  Any
  * K >= 1; M, K <= 2^30, M * K <= 2^40.  Rows are contiguous ([M, K] row-major); K % 8 == 0

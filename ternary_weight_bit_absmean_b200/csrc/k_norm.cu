@@ -13,8 +13,17 @@
 //
 // The backward takes mu and r from x again instead of reading saved ones: the row is on
 // chip anyway for n.  All sums are fp32: a thread adds its elements in order, the threads
-// of a row add in a tree, and the squares are of the already centred values, so a large
-// mean costs no digits.
+// of a row add in a tree.
+//
+// Layer kind: a mean from a plain fp32 sum is some units in its last place off, which for
+// |mean| >> sigma shifts every n of the row by error / sigma (1e4 + 0.1 N(0,1), K = 3200: 8e-3).
+// So the sum runs over x - ref, with ref the mean of four neighbouring elements of the row, and
+//   mu + lo = ref + mean_k (x - ref),  c = x - mu,  n = (c - lo) r,
+//   mean_k (x - mean)^2 = mean_k c^2 - lo^2,   mean_k(g n) = (mean_k(g c) - lo mean_k g) r
+// where lo is what rounding the mean to fp32 leaves over.  The differences are right to half a unit
+// of their own, so what is left is the rounding of a sum of them, whatever the mean; a constant
+// row's are all zero.  Cost: one subtraction an element (8192 x 8192 bf16 with a bias: forward 52.0
+// -> 54.5 us, backward 113.5 -> 116.2).
 //
 // Both are bound by memory: a row is read once, held in registers as it came, and written once.
 // A matrix is cut into chunks of eight elements of its flat order, whatever K is, so that every
@@ -76,6 +85,10 @@ struct Raw;
 template <>
 struct Raw<float> {
     float4 a, b;
+    // what the compiler cannot see through: the values are converted and used from here, not held
+    __device__ __forceinline__ void pin() {
+        asm volatile("" : "+f"(a.x), "+f"(a.y), "+f"(a.z), "+f"(a.w), "+f"(b.x), "+f"(b.y), "+f"(b.z), "+f"(b.w));
+    }
     __device__ __forceinline__ void load(const float* p) {
         a = *reinterpret_cast<const float4*>(p);
         b = *reinterpret_cast<const float4*>(p + 4);
@@ -112,6 +125,7 @@ struct Raw<float> {
 template <>
 struct Raw<__nv_bfloat16> {
     uint4 a;
+    __device__ __forceinline__ void pin() { asm volatile("" : "+r"(a.x), "+r"(a.y), "+r"(a.z), "+r"(a.w)); }
     __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = *reinterpret_cast<const uint4*>(p); }
     __device__ __forceinline__ void load_global(const __nv_bfloat16* p) {
         a = __ldg(reinterpret_cast<const uint4*>(p));
@@ -131,6 +145,56 @@ struct Raw<__nv_bfloat16> {
         return __uint_as_float((e & 1) ? (w & 0xFFFF0000u) : (w << 16));
     }
 };
+
+// The mean of four elements, exact if they are one value.
+__device__ __forceinline__ float mean_of(float a, float b, float c, float d) {
+    return fmaf(a, 0.25f, 0.25f * b) + fmaf(c, 0.25f, 0.25f * d);
+}
+__device__ __forceinline__ float mean_of(const float4& v) { return mean_of(v.x, v.y, v.z, v.w); }
+__device__ __forceinline__ float mean_of(const uint2& v) {  // bf16
+    return mean_of(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u), __uint_as_float(v.y << 16),
+                   __uint_as_float(v.y & 0xFFFF0000u));
+}
+template <typename T>
+struct Four;
+template <>
+struct Four<float> {
+    using Type = float4;
+};
+template <>
+struct Four<__nv_bfloat16> {
+    using Type = uint2;
+};
+
+// What the layer kind's sums are taken from (see the top): the mean of the first four elements of a
+// row of n that lie on their own alignment, or its first element where no four do.  The row starts
+// `skip` elements behind a chunk's start.
+template <typename T>
+__device__ __forceinline__ float reference(const T* row, int skip, int64_t n) {
+    const int ahead = -skip & 3;
+    if (ahead + 4 > n) return to_f32(row[0]);
+    return mean_of(*reinterpret_cast<const typename Four<T>::Type*>(row + ahead));
+}
+
+// ref + delta in two parts: the rounded sum and what that leaves over.
+struct Mean {
+    float mu, lo;
+};
+__device__ __forceinline__ Mean mean_from(float ref, float delta) {
+    const float mu = ref + delta, b = mu - ref;
+    return Mean{mu, (ref - (mu - b)) + (delta - b)};
+}
+
+// 1 / sqrt(variance + eps) from the sum of c^2, and shift with n = c r + shift.  (Without a mean
+// lo is 0, and adding -0 changes no value.)
+struct Spread {
+    float r, shift;
+};
+__device__ __forceinline__ Spread spread_of(bool layer, float sum_cc, float lo, float inv_k, float eps) {
+    if (!layer) return Spread{__frsqrt_rn(fmaf(sum_cc, inv_k, eps)), -0.0f};
+    const float r = __frsqrt_rn(fmaf(-lo, lo, sum_cc * inv_k) + eps);
+    return Spread{r, -lo * r};
+}
 
 // A chunk of the output at flat element `flat`, as fp32 or bf16.
 __device__ __forceinline__ void store_flat(void* out, bool bf16, int64_t flat, const Mask& m, const float (&v)[kE]) {
@@ -300,25 +364,35 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_forward_kernel(const TX*
         for (int e = 0; e < kE; ++e) v[e] = x[r][c][e];
     };
     // both of the sums that GroupSum takes are of rows: row 0 and row R - 1
-    float mu[R], rstd[R];
+    float mu[R], lo[R];
 #pragma unroll
-    for (int r = 0; r < R; ++r) mu[r] = 0.0f;
+    for (int r = 0; r < R; ++r) mu[r] = lo[r] = 0.0f;
     if (a.layer) {
-        float s[R];
+        float s[R], ref[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
+            ref[r] = R == 1 || m0 + r < a.M ? reference(X + (m0 + r) * a.K, EDGE ? skip(r) : 0, a.K) : 0.0f;
             s[r] = 0.0f;
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
+                const Mask k = mask(r, c);
                 float v[kE];
                 values(r, c, v);
+                const float from = k.any() ? ref[r] : 0.0f;  // a chunk that is not the row's is zeros
+#pragma unroll
+                for (int e = 0; e < kE; ++e) v[e] -= from;
+                if (EDGE && !k.all())
+#pragma unroll
+                    for (int e = 0; e < kE; ++e)
+                        if (!k.has(e)) v[e] = 0.0f;
 #pragma unroll
                 for (int e = 0; e < kE; ++e) s[r] += v[e];
             }
         }
         const float2 both = row_sum(s[0], R > 1 ? s[R - 1] : 0.0f);
-        mu[0] = both.x * a.inv_k;
-        if constexpr (R > 1) mu[1] = both.y * a.inv_k;
+        const Mean first = mean_from(ref[0], both.x * a.inv_k), second = mean_from(ref[R - 1], both.y * a.inv_k);
+        mu[0] = first.mu, lo[0] = first.lo;
+        if constexpr (R > 1) mu[1] = second.mu, lo[1] = second.lo;
     }
     float q[R];
 #pragma unroll
@@ -341,8 +415,9 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_forward_kernel(const TX*
         }
     }
     const float2 both = row_sum(q[0], R > 1 ? q[R - 1] : 0.0f);
-    rstd[0] = __frsqrt_rn(fmaf(both.x, a.inv_k, a.eps));
-    if constexpr (R > 1) rstd[1] = __frsqrt_rn(fmaf(both.y, a.inv_k, a.eps));
+    Spread of[R];
+    of[0] = spread_of(a.layer, both.x, lo[0], a.inv_k, a.eps);
+    if constexpr (R > 1) of[1] = spread_of(a.layer, both.y, lo[1], a.inv_k, a.eps);
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
         float w[kE], b[kE];
@@ -357,7 +432,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) norm_forward_kernel(const TX*
             float v[kE];
             values(r, c, v);
 #pragma unroll
-            for (int e = 0; e < kE; ++e) v[e] = (v[e] - mu[r]) * rstd[r] * w[e] + b[e];
+            for (int e = 0; e < kE; ++e) v[e] = fmaf(v[e] - mu[r], of[r].r, of[r].shift) * w[e] + b[e];
             store_flat(a.out, a.out_bf16, flat(r, c), k, v);
         }
     }
@@ -399,20 +474,22 @@ __global__ void __launch_bounds__(kMaxThreads) norm_forward_long_kernel(const TX
     BlockSum row_sum{sums, t, tpr};
     const int64_t m = blockIdx.x;
     const TX* row = X + m * a.K;
-    float mu = 0.0f;
+    float mu = 0.0f, lo = 0.0f;
     if (a.layer) {
+        const float ref = reference(row, static_cast<int>(m * a.K & (kE - 1)), a.K);
         float s = 0.0f;
-        for (int64_t k = t; k < a.K; k += tpr) s += to_f32(row[k]);
-        mu = row_sum(s, 0.0f).x * a.inv_k;
+        for (int64_t k = t; k < a.K; k += tpr) s += to_f32(row[k]) - ref;
+        const Mean mean = mean_from(ref, row_sum(s, 0.0f).x * a.inv_k);
+        mu = mean.mu, lo = mean.lo;
     }
     float v = 0.0f;
     for (int64_t k = t; k < a.K; k += tpr) {
         const float d = to_f32(row[k]) - mu;
         v = fmaf(d, d, v);
     }
-    const float r = __frsqrt_rn(fmaf(row_sum(v, 0.0f).x, a.inv_k, a.eps));
+    const Spread of = spread_of(a.layer, row_sum(v, 0.0f).x, lo, a.inv_k, a.eps);
     for (int64_t k = t; k < a.K; k += tpr) {
-        float y = (to_f32(row[k]) - mu) * r;
+        float y = fmaf(to_f32(row[k]) - mu, of.r, of.shift);
         if (a.w != nullptr) y *= __ldg(a.w + k);
         if (a.b != nullptr) y += __ldg(a.b + k);
         if (a.out_bf16)
@@ -445,7 +522,7 @@ struct Shape {
 struct Control {
     uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t cross[2];                    // row sums of the blocks of the cluster
-    float2 cross_sums[2][kMaxCluster];
+    float4 cross_sums[2][kMaxCluster];
     float2 sums[kMaxGroups][64];
     int abort;
 };
@@ -462,24 +539,46 @@ struct RowSum {
         const uint32_t call = local.calls;
         const float2 own = local(a, b);
         if (cluster == 1) return own;
+        exchange(call, make_float4(own.x, own.y, 0.0f, 0.0f));
+        float2 all = make_float2(0.0f, 0.0f);
+        for (int i = 0; i < cluster; ++i) {
+            const float4 v = ctl->cross_sums[call & 1][i];
+            all.x += v.x, all.y += v.y;
+        }
+        return all;
+    }
+    // The same where a is a sum over this block's `slice` columns (the last block's: the rest of K)
+    // of differences from its own ref: returns their sum from the first block's ref, and that.
+    __device__ __forceinline__ float3 from_ref(float a, float b, float ref, int slice, int64_t K) {
+        const uint32_t call = local.calls;
+        const float2 own = local(a, b);
+        if (cluster == 1) return make_float3(own.x, own.y, ref);
+        exchange(call, make_float4(own.x, own.y, ref, 0.0f));
+        const float4* s = ctl->cross_sums[call & 1];
+        const float first = s[0].z;
+        float2 all = make_float2(0.0f, 0.0f);
+        for (int i = 0; i < cluster; ++i) {
+            const float4 v = s[i];
+            const float n = static_cast<float>(i + 1 < cluster ? slice : static_cast<int>(K - int64_t(i) * slice));
+            all.x += fmaf(n, v.z - first, v.x);
+            all.y += v.y;
+        }
+        return make_float3(all.x, all.y, first);
+    }
+    __device__ __forceinline__ void exchange(uint32_t call, const float4& own) {
         const int slot = static_cast<int>(call & 1), t = local.t;
         const uint32_t bar = smem_u32(&ctl->cross[slot]);
-        if (t == 0) mbar_arrive_expect_tx(bar, 8u * static_cast<uint32_t>(cluster));
+        if (t == 0) mbar_arrive_expect_tx(bar, 16u * static_cast<uint32_t>(cluster));
         if (t < cluster) {
             const uint32_t dst = mapa_shared(smem_u32(&ctl->cross_sums[slot][rank]), static_cast<uint32_t>(t));
             const uint32_t rbar = mapa_shared(bar, static_cast<uint32_t>(t));
             asm volatile(
-                "st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];" ::"r"(dst),
-                "r"(__float_as_uint(own.x)), "r"(__float_as_uint(own.y)), "r"(rbar)
+                "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(dst),
+                "r"(__float_as_uint(own.x)), "r"(__float_as_uint(own.y)), "r"(__float_as_uint(own.z)),
+                "r"(__float_as_uint(own.w)), "r"(rbar)
                 : "memory");
         }
         mbar_wait_bounded(bar, (call >> 1) & 1u, &ctl->abort);
-        float2 all = make_float2(0.0f, 0.0f);
-        for (int i = 0; i < cluster; ++i) {
-            all.x += ctl->cross_sums[slot][i].x;
-            all.y += ctl->cross_sums[slot][i].y;
-        }
-        return all;
     }
 };
 
@@ -595,7 +694,6 @@ __device__ __forceinline__ void fill_ring(const Place& pl, const Shape& s, const
 struct BwdArgs {
     Shape s;
     const float* w;
-    bool layer;
     float eps, inv_k;
     void* dx;
     bool dx_bf16;
@@ -604,8 +702,9 @@ struct BwdArgs {
     int32_t* err;
 };
 
-// DB: with the bias's gradient (its sums take registers).
-template <typename TX, typename TD, bool EDGE, bool DB, int CH, int THREADS>
+// LAYER: the kind, known when compiling, so that RMS rows pay nothing for the mean (8192 x 8640: 121
+// us, with a test at run time 145).  DB: with the bias's gradient (its sums take registers).
+template <typename TX, typename TD, bool EDGE, bool LAYER, bool DB, int CH, int THREADS>
 __global__ void __launch_bounds__(THREADS)
     norm_backward_kernel(const TX* __restrict__ X, const TD* __restrict__ dY, const __grid_constant__ BwdArgs a) {
     extern __shared__ __align__(128) uint8_t smem[];
@@ -645,6 +744,15 @@ __global__ void __launch_bounds__(THREADS)
         // values converted once with one chunk; with two that costs more (123 -> 133 us for 8192 x
         // 8640 RMS), and the raw chunk is converted in each pass
         constexpr bool kOnce = CH == 1;
+        // Two chunks, both gradients and both sums in 96 registers: held from one pass to the next, the
+        // converted values spill (8192 x 4096 bf16 114 us against 72, 8192 x 8640 bf16 x, fp32 dy 287
+        // against 218), so each pass starts from the raw chunks, and addresses from the row.
+        constexpr bool kTight = LAYER && DB && THREADS == 640;
+        auto drop = [&](Raw<TX>(&x)[CH], Raw<TD>(&d)[CH]) {
+            if constexpr (kTight)
+#pragma unroll
+                for (int c = 0; c < CH; ++c) x[c].pin(), d[c].pin();
+        };
         int stage = 0;
         uint32_t phase = 0;
         for (int64_t m = pl.first + pl.group; m - pl.group < s.M; m += pl.step, flat += flat_step) {
@@ -666,6 +774,10 @@ __global__ void __launch_bounds__(THREADS)
                     d[c].clear();
                 }
             }
+            float ref = 0.0f;
+            if (LAYER && live) {  // here as well: the slot is given back below
+                ref = reference(reinterpret_cast<const TX*>(slot) + at - t * kE + skip, EDGE ? skip : 0, pl.ks);
+            }
             __syncwarp();
             if ((t & 31) == 0) mbar_arrive(smem_u32(&pl.ctl->empty[stage]));
             if (++stage == s.stages) {
@@ -673,14 +785,14 @@ __global__ void __launch_bounds__(THREADS)
                 phase ^= 1u;
             }
             if (!live) continue;  // rows of a batch past the last one: the whole group skips
-            // the values of chunk c, zero where they are not the row's
+            // the values of chunk c; where they are not the row's, x is ref and dy zero
             auto convert = [&](int c, float(&xv)[kE], float(&dv)[kE]) {
 #pragma unroll
                 for (int e = 0; e < kE; ++e) xv[e] = x[c][e], dv[e] = d[c][e];
                 if (EDGE && !mask[c].all())
 #pragma unroll
                     for (int e = 0; e < kE; ++e)
-                        if (!mask[c].has(e)) xv[e] = dv[e] = 0.0f;
+                        if (!mask[c].has(e)) xv[e] = ref, dv[e] = 0.0f;
             };
             float xs[kOnce ? CH : 1][kE], ds[kOnce ? CH : 1][kE];
             if constexpr (kOnce)
@@ -694,22 +806,25 @@ __global__ void __launch_bounds__(THREADS)
                     convert(c, xv, dv);
                 }
             };
-            float mu = 0.0f, c2 = 0.0f;
-            if (a.layer) {
+            float mu = 0.0f, lo = 0.0f, c2 = 0.0f;
+            if constexpr (LAYER) {
                 float sum = 0.0f, sg = 0.0f;
 #pragma unroll
                 for (int c = 0; c < CH; ++c) {
                     float xv[kE], dv[kE];
                     values(c, xv, dv);
+                    const float from = EDGE || mask[c].any() ? ref : 0.0f;  // a chunk that is not the row's is zeros
 #pragma unroll
                     for (int e = 0; e < kE; ++e) {
-                        sum += xv[e];
+                        sum += xv[e] - from;
                         sg = fmaf(dv[e], w[c][e], sg);
                     }
                 }
-                const float2 both = row_sum(sum, sg);
-                mu = both.x * a.inv_k;
-                c2 = both.y * a.inv_k;
+                const float3 all = row_sum.from_ref(sum, sg, ref, s.slice, s.K);
+                const Mean mean = mean_from(all.z, all.x * a.inv_k);
+                mu = mean.mu, lo = mean.lo;
+                c2 = all.y * a.inv_k;
+                drop(x, d);
             }
             float v = 0.0f, gx = 0.0f;
 #pragma unroll
@@ -723,6 +838,9 @@ __global__ void __launch_bounds__(THREADS)
 #pragma unroll
                     for (int e = 0; e < kE; ++e)
                         if (!mask[c].has(e)) xv[e] = 0.0f;
+                if constexpr (kOnce)
+#pragma unroll
+                    for (int e = 0; e < kE; ++e) xs[c][e] = xv[e];
 #pragma unroll
                 for (int e = 0; e < kE; ++e) {
                     v = fmaf(xv[e], xv[e], v);
@@ -730,8 +848,10 @@ __global__ void __launch_bounds__(THREADS)
                 }
             }
             const float2 both = row_sum(v, gx);
-            const float r = __frsqrt_rn(fmaf(both.x, a.inv_k, a.eps));
-            const float c1 = both.y * a.inv_k * r;
+            drop(x, d);
+            const Spread of = spread_of(LAYER, both.x, lo, a.inv_k, a.eps);
+            const float r = of.r;
+            const float c1 = fmaf(-lo, c2, both.y * a.inv_k) * r;
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
                 if (!mask[c].any()) continue;
@@ -739,12 +859,13 @@ __global__ void __launch_bounds__(THREADS)
                 values(c, xv, dv);
 #pragma unroll
                 for (int e = 0; e < kE; ++e) {
-                    const float n = (xv[e] - mu) * r;
+                    const float n = fmaf(kOnce ? xv[e] : xv[e] - mu, r, of.shift);
                     dw[c][e] = fmaf(dv[e], n, dw[c][e]);
                     if constexpr (DB) db[c][e] += dv[e];
                     xv[e] = r * fmaf(-n, c1, fmaf(dv[e], w[c][e], -c2));
                 }
-                store_flat(a.dx, a.dx_bf16, flat + c * tpr * kE, mask[c], xv);
+                const int64_t first = kTight ? m * s.K + (pl.k0 - skip + t * kE) : flat;
+                store_flat(a.dx, a.dx_bf16, first + c * tpr * kE, mask[c], xv);
             }
         }
     }
@@ -803,11 +924,11 @@ struct LongBwdArgs {
 };
 
 // Rows longer than a cluster's slices: dx row by row as in norm_forward_long_kernel, keeping
-// (mu, r) of every row for the column kernel below.
+// (mu, r, shift) of every row for the column kernel below.
 template <typename TX, typename TD>
 __global__ void __launch_bounds__(kMaxThreads)
     norm_backward_long_kernel(const TX* __restrict__ X, const TD* __restrict__ dY, const LongBwdArgs a,
-                              float2* __restrict__ stats) {
+                              float4* __restrict__ stats) {
     __shared__ float2 sums[64];
     const int t = threadIdx.x, tpr = blockDim.x;
     pdl_wait_then_release();
@@ -819,15 +940,17 @@ __global__ void __launch_bounds__(kMaxThreads)
         const float d = to_f32(drow[k]);
         return a.w != nullptr ? d * __ldg(a.w + k) : d;
     };
-    float mu = 0.0f, c2 = 0.0f;
+    float mu = 0.0f, lo = 0.0f, c2 = 0.0f;
     if (a.layer) {
+        const float ref = reference(row, static_cast<int>(m * a.K & (kE - 1)), a.K);
         float s = 0.0f, sg = 0.0f;
         for (int64_t k = t; k < a.K; k += tpr) {
-            s += to_f32(row[k]);
+            s += to_f32(row[k]) - ref;
             sg += grad(k);
         }
         const float2 both = row_sum(s, sg);
-        mu = both.x * a.inv_k;
+        const Mean mean = mean_from(ref, both.x * a.inv_k);
+        mu = mean.mu, lo = mean.lo;
         c2 = both.y * a.inv_k;
     }
     float v = 0.0f, gx = 0.0f;
@@ -837,24 +960,24 @@ __global__ void __launch_bounds__(kMaxThreads)
         gx = fmaf(grad(k), x, gx);
     }
     const float2 both = row_sum(v, gx);
-    const float r = __frsqrt_rn(fmaf(both.x, a.inv_k, a.eps));
-    const float c1 = both.y * a.inv_k * r;
+    const Spread of = spread_of(a.layer, both.x, lo, a.inv_k, a.eps);
+    const float c1 = fmaf(-lo, c2, both.y * a.inv_k) * of.r;
     for (int64_t k = t; k < a.K; k += tpr) {
-        const float n = (to_f32(row[k]) - mu) * r;
-        const float o = r * ((grad(k) - c2) - n * c1);
+        const float n = fmaf(to_f32(row[k]) - mu, of.r, of.shift);
+        const float o = of.r * ((grad(k) - c2) - n * c1);
         if (a.dx_bf16)
             static_cast<__nv_bfloat16*>(a.dx)[m * a.K + k] = __float2bfloat16_rn(o);
         else
             static_cast<float*>(a.dx)[m * a.K + k] = o;
     }
-    if (t == 0 && stats != nullptr) stats[m] = make_float2(mu, r);
+    if (t == 0 && stats != nullptr) stats[m] = make_float4(mu, of.r, of.shift, 0.0f);
 }
 
-// Column sums of a strip of rows from x, dy and the rows' (mu, r): a thread owns a column.
+// Column sums of a strip of rows from x, dy and the rows' (mu, r, shift): a thread owns a column.
 template <typename TX, typename TD>
 __global__ void __launch_bounds__(256)
     norm_columns_long_kernel(const TX* __restrict__ X, const TD* __restrict__ dY, const LongBwdArgs a,
-                             const float2* __restrict__ stats, int64_t rows_per_block) {
+                             const float4* __restrict__ stats, int64_t rows_per_block) {
     pdl_wait_then_release();
     const int64_t m0 = blockIdx.x * rows_per_block;
     const int64_t m1 = m0 + rows_per_block < a.M ? m0 + rows_per_block : a.M;
@@ -862,9 +985,9 @@ __global__ void __launch_bounds__(256)
         float dw = 0.0f, db = 0.0f;
 #pragma unroll 4
         for (int64_t m = m0; m < m1; ++m) {
-            const float2 st = __ldg(stats + m);
+            const float4 st = __ldg(stats + m);
             const float d = to_f32(dY[m * a.K + k]);
-            dw = fmaf(d, (to_f32(X[m * a.K + k]) - st.x) * st.y, dw);
+            dw = fmaf(d, fmaf(to_f32(X[m * a.K + k]) - st.x, st.y, st.z), dw);
             db += d;
         }
         if (a.dw != nullptr) a.dw[blockIdx.x * a.K + k] = dw;
@@ -1010,15 +1133,15 @@ int backward_parts(int64_t M, int64_t K) {
     return static_cast<int>(strips < kParts ? strips : kParts);
 }
 
-template <typename TX, typename TD, bool EDGE, bool DB, int CH, int THREADS>
+template <typename TX, typename TD, bool EDGE, bool LAYER, bool DB, int CH, int THREADS>
 cudaError_t backward_c(const TX* X, const TD* dY, const Plan& p, const BwdArgs& a, cudaStream_t stream) {
     static PerContextOnce attr;
     cudaError_t e = attr.run([] {
-        return cudaFuncSetAttribute(norm_backward_kernel<TX, TD, EDGE, DB, CH, THREADS>,
+        return cudaFuncSetAttribute(norm_backward_kernel<TX, TD, EDGE, LAYER, DB, CH, THREADS>,
                                     cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost);
     });
     if (e != cudaSuccess) return e;
-    return launch_pdl(norm_backward_kernel<TX, TD, EDGE, DB, CH, THREADS>,
+    return launch_pdl(norm_backward_kernel<TX, TD, EDGE, LAYER, DB, CH, THREADS>,
                       dim3(static_cast<unsigned>(p.parts * p.cluster)), dim3(p.s.tpr * p.s.groups + 32), smem_of(p), stream,
                       p.cluster > 1 ? dim3(p.cluster, 1, 1) : dim3(kNoCluster), X, dY, a);
 }
@@ -1027,21 +1150,21 @@ cudaError_t backward_c(const TX* X, const TD* dY, const Plan& p, const BwdArgs& 
 // 168 with up to 384 (8192 x 7680 layer fp32 at 128 registers 134 us, at the 96 of 640 threads 210).
 // Without a bias 96 do, and what more there is only lets the compiler move loads (8192 x 7680 RMS:
 // 104 against 116 us).
-template <typename TX, typename TD, bool EDGE>
+template <typename TX, typename TD, bool EDGE, bool LAYER>
 cudaError_t backward_e(const TX* X, const TD* dY, const Plan& p, const BwdArgs& a, cudaStream_t stream) {
     if (a.db != nullptr) {
         if (p.chunks == 1)
-            return p.s.tpr * p.s.groups < 768 ? backward_c<TX, TD, EDGE, true, 1, 768>(X, dY, p, a, stream)
-                                              : backward_c<TX, TD, EDGE, true, 1, 800>(X, dY, p, a, stream);
-        if (p.chunks == 3) return backward_c<TX, TD, EDGE, true, 3, 384>(X, dY, p, a, stream);
-        if (p.s.tpr * p.s.groups < 512) return backward_c<TX, TD, EDGE, true, 2, 512>(X, dY, p, a, stream);
-        return backward_c<TX, TD, EDGE, true, 2, 640>(X, dY, p, a, stream);
+            return p.s.tpr * p.s.groups < 768 ? backward_c<TX, TD, EDGE, LAYER, true, 1, 768>(X, dY, p, a, stream)
+                                              : backward_c<TX, TD, EDGE, LAYER, true, 1, 800>(X, dY, p, a, stream);
+        if (p.chunks == 3) return backward_c<TX, TD, EDGE, LAYER, true, 3, 384>(X, dY, p, a, stream);
+        if (p.s.tpr * p.s.groups < 512) return backward_c<TX, TD, EDGE, LAYER, true, 2, 512>(X, dY, p, a, stream);
+        return backward_c<TX, TD, EDGE, LAYER, true, 2, 640>(X, dY, p, a, stream);
     }
     if (p.chunks == 1)
-        return p.s.tpr * p.s.groups < 768 ? backward_c<TX, TD, EDGE, false, 1, 768>(X, dY, p, a, stream)
-                                          : backward_c<TX, TD, EDGE, false, 1, 800>(X, dY, p, a, stream);
-    if (p.chunks == 3) return backward_c<TX, TD, EDGE, false, 3, 384>(X, dY, p, a, stream);
-    return backward_c<TX, TD, EDGE, false, 2, 640>(X, dY, p, a, stream);
+        return p.s.tpr * p.s.groups < 768 ? backward_c<TX, TD, EDGE, LAYER, false, 1, 768>(X, dY, p, a, stream)
+                                          : backward_c<TX, TD, EDGE, LAYER, false, 1, 800>(X, dY, p, a, stream);
+    if (p.chunks == 3) return backward_c<TX, TD, EDGE, LAYER, false, 3, 384>(X, dY, p, a, stream);
+    return backward_c<TX, TD, EDGE, LAYER, false, 2, 640>(X, dY, p, a, stream);
 }
 
 struct BwdCall {
@@ -1053,7 +1176,7 @@ struct BwdCall {
     bool dx_bf16;
     float* dw;  // where the kernels leave their sums: partial ones with several parts
     float* db;
-    float2* stats;
+    float4* stats;
     int parts;
     int32_t* err;
 };
@@ -1070,12 +1193,15 @@ cudaError_t backward_t(const TX* X, const TD* dY, const BwdCall& c, cudaStream_t
         const int64_t strips = (c.K + 255) / 256;
         return launch_pdl(norm_columns_long_kernel<TX, TD>,
                           dim3(c.parts, static_cast<unsigned>(strips < 65535 ? strips : 65535)), dim3(256), 0, stream,
-                          dim3(kNoCluster), X, dY, a, static_cast<const float2*>(c.stats), rows);
+                          dim3(kNoCluster), X, dY, a, static_cast<const float4*>(c.stats), rows);
     }
     const Plan p = plan_of(c.M, c.K, sizeof(TX), sizeof(TD));
-    const BwdArgs a{p.s, c.w, c.layer, c.eps, inv_k, c.dx, c.dx_bf16, c.dw, c.db, c.err};
-    return c.K % kE == 0 ? backward_e<TX, TD, false>(X, dY, p, a, stream)
-                         : backward_e<TX, TD, true>(X, dY, p, a, stream);
+    const BwdArgs a{p.s, c.w, c.eps, inv_k, c.dx, c.dx_bf16, c.dw, c.db, c.err};
+    if (c.K % kE == 0)
+        return c.layer ? backward_e<TX, TD, false, true>(X, dY, p, a, stream)
+                       : backward_e<TX, TD, false, false>(X, dY, p, a, stream);
+    return c.layer ? backward_e<TX, TD, true, true>(X, dY, p, a, stream)
+                   : backward_e<TX, TD, true, false>(X, dY, p, a, stream);
 }
 
 int64_t align16(int64_t n) { return (n + 15) / 16 * 16; }
@@ -1093,7 +1219,7 @@ cudaError_t launch_norm_forward(const void* X, bool x_bf16, const float* w, cons
 size_t norm_backward_workspace(int64_t M, int64_t K) {
     const int64_t parts = backward_parts(M, K);
     int64_t bytes = parts > 1 ? 2 * align16(parts * K * 4) : 0;
-    if (is_long(K)) bytes += align16(M * 8);
+    if (is_long(K)) bytes += 16 * M;
     return static_cast<size_t>(bytes);
 }
 
@@ -1109,7 +1235,7 @@ cudaError_t launch_norm_backward(const void* dY, bool dy_bf16, const void* X, bo
         if (db != nullptr) c.db = reinterpret_cast<float*>(p + part_bytes);
         p += 2 * part_bytes;
     }
-    if (is_long(K)) c.stats = reinterpret_cast<float2*>(p);
+    if (is_long(K)) c.stats = reinterpret_cast<float4*>(p);
     cudaError_t e;
     if (x_bf16) {
         const auto* x = static_cast<const __nv_bfloat16*>(X);
