@@ -489,6 +489,19 @@ BL_API bl_status bitlinear_fp8_forward(const uint8_t *xq, const float *sx, const
                                        int64_t M, int64_t N, int64_t K, void *out, bl_dtype out_dtype,
                                        int32_t *err_word, void *stream);
 
+/* A test of the products' bounded device waits: bitlinear_fp8_forward in which every wait
+ * gives up after wait_limit_ns (0 < wait_limit_ns <= 2 s; the products use 2 s) and the load
+ * producer of each block stops after stall_after_loads loads.  The waits for the next load then
+ * run out: the kernel ends its other roles, waits for every copy and MMA in flight, frees its
+ * tensor memory, ORs BL_ERRBIT_TIMEOUT into err_word and returns; the output is left
+ * incomplete.  If no block needs more loads than stall_after_loads it finishes normally.  The
+ * next call on the stream runs as usual.  The three products run the same kernels.
+ * Errors: those of bitlinear_fp8_forward; BL_ERR_INVALID_ARG for a limit out of range. */
+BL_API bl_status bitlinear_fp8_stall_test(const uint8_t *xq, const float *sx, const uint8_t *wq, const float *sw,
+                                          int64_t M, int64_t N, int64_t K, void *out, bl_dtype out_dtype,
+                                          int32_t *err_word, uint64_t wait_limit_ns, int32_t stall_after_loads,
+                                          void *stream);
+
 /* dX[m, k] = sum_n dY[m, n] w[n, k] from codes.
  *   dyq, sdy in : the gradient's codes [M, row_bytes(N)] and scales [ceil(N / 128), M].
  *   wqt, sw  in : transposed weight codes [K, row_bytes(N)] and the weights' scales.

@@ -39,6 +39,7 @@ EXPORTED = [
     "bitlinear_norm_forward", "bitlinear_norm_backward_workspace_size", "bitlinear_norm_backward",
     "bitlinear_fp8_row_bytes", "bitlinear_fp8_quantize_act", "bitlinear_fp8_quantize_weights",
     "bitlinear_fp8_forward", "bitlinear_fp8_backward_input", "bitlinear_fp8_backward_weight",
+    "bitlinear_fp8_stall_test",
     "bitlinear_last_cuda_error",
     "bitlinear_status_string",
 ]
@@ -118,6 +119,8 @@ def lib() -> ctypes.CDLL:
         L.bitlinear_fp8_quantize_weights.restype = S
         L.bitlinear_fp8_forward.argtypes = [P, P, P, P, I64, I64, I64, P, S, P, P]
         L.bitlinear_fp8_forward.restype = S
+        L.bitlinear_fp8_stall_test.argtypes = [P, P, P, P, I64, I64, I64, P, S, P, ctypes.c_uint64, ctypes.c_int32, P]
+        L.bitlinear_fp8_stall_test.restype = S
         L.bitlinear_fp8_backward_input.argtypes = [P, P, P, P, I64, I64, I64, P, S, P, P]
         L.bitlinear_fp8_backward_input.restype = S
         L.bitlinear_fp8_backward_weight.argtypes = [P, P, P, P, I64, I64, I64, P, S, P, P]
@@ -472,6 +475,18 @@ def bitlinear_fp8_forward(xq, sx, wq, sw, out, err_word=None):
         _ptr(xq, _E4M3, "xq"), _ptr(sx, torch.float32, "sx", (_blocks(K), M)), _ptr(wq, _E4M3, "wq"),
         _ptr(sw, torch.float32, "sw", (_blocks(N), _blocks(K))), M, N, K, *_float(out, "out", (M, N)),
         _opt(err_word, "err_word"), _here(xq)), "bitlinear_fp8_forward")
+
+
+@_scoped
+def bitlinear_fp8_stall_test(xq, sx, wq, sw, out, err_word, wait_limit_ns, stall_after_loads):
+    """The product with every device wait limited to wait_limit_ns and each block's load
+    producer stopped after stall_after_loads loads (a test of the bounded waits)."""
+    M, N, K = _codes_of(xq, wq, ("xq", "wq"))
+    _check(lib().bitlinear_fp8_stall_test(
+        _ptr(xq, _E4M3, "xq"), _ptr(sx, torch.float32, "sx", (_blocks(K), M)), _ptr(wq, _E4M3, "wq"),
+        _ptr(sw, torch.float32, "sw", (_blocks(N), _blocks(K))), M, N, K, *_float(out, "out", (M, N)),
+        _opt(err_word, "err_word"), int(wait_limit_ns), int(stall_after_loads), _here(xq)),
+        "bitlinear_fp8_stall_test")
 
 
 @_scoped

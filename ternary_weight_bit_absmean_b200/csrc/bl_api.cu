@@ -460,6 +460,18 @@ bl_status bitlinear_fp8_forward(const uint8_t* xq, const float* sx, const uint8_
     return fp8_product(xq, sx, wq, sw, M, N, K, (K + 127) / 128, 1, 7, out, out_dtype, err_word, stream);
 }
 
+bl_status bitlinear_fp8_stall_test(const uint8_t* xq, const float* sx, const uint8_t* wq, const float* sw, int64_t M,
+                                   int64_t N, int64_t K, void* out, bl_dtype out_dtype, int32_t* err_word,
+                                   uint64_t wait_limit_ns, int32_t stall_after_loads, void* stream) {
+    BL_RANGE("bitlinear_fp8_stall_test");
+    if (wait_limit_ns == 0 || wait_limit_ns > bl::kDefaultWaitNs || stall_after_loads < 0) return BL_ERR_INVALID_ARG;
+    const bl::WaitTest saved = bl::g_wait_test;
+    bl::g_wait_test = bl::WaitTest{wait_limit_ns, stall_after_loads};
+    const bl_status st = bitlinear_fp8_forward(xq, sx, wq, sw, M, N, K, out, out_dtype, err_word, stream);
+    bl::g_wait_test = saved;
+    return st;
+}
+
 bl_status bitlinear_fp8_backward_input(const uint8_t* dyq, const float* sdy, const uint8_t* wqt, const float* sw,
                                        int64_t M, int64_t N, int64_t K, void* dX, bl_dtype out_dtype,
                                        int32_t* err_word, void* stream) {

@@ -21,8 +21,9 @@
 //                      the BQ columns.
 // With few tiles the groups are split over the blocks of a cluster, which add their
 // partial sums through distributed shared memory in a fixed order.  All waits are bounded
-// as in the ternary kernels; a block that gives up drains its copies and MMAs, sets
-// BL_ERRBIT_TIMEOUT and still takes part in the cluster barriers.
+// as in the ternary kernels; a block that gives up (see bl_fp8.cuh) lets its roles run out,
+// waits for its loads and MMAs in flight, sets BL_ERRBIT_TIMEOUT and still takes part in the
+// cluster barriers.
 #include <algorithm>
 #include <cmath>
 #include <cuda_bf16.h>
@@ -37,8 +38,6 @@
 
 namespace bl {
 
-// 2-D tensor map over rows of `inner` bytes that start every `pitch` bytes, 128-byte
-// swizzle, zero fill outside; encoded anew by every call.
 bool encode_tmap_u8_pitch(CUtensorMap* map, const void* ptr, uint64_t inner, uint64_t outer, uint64_t pitch,
                           uint32_t box_inner, uint32_t box_outer) {
     struct Encode {
@@ -70,7 +69,6 @@ constexpr int kG = 128;     // contraction elements (bytes) per group and stage
 constexpr int kWarpTma = 0, kWarpMma = 1, kWarpScale = 2, kWarpEpi = 4;
 constexpr int kScaleSlots = 8;
 constexpr int kMaxCluster = 8;
-constexpr unsigned long long kDrainNs = 200000000ull;  // 0.2 s
 
 template <int BQ>
 struct Cfg {
@@ -99,14 +97,9 @@ struct Args {
     int groups;            // of the contraction
     int groups_per_split;  // of a block of the cluster (the last takes the rest)
     int tiles_q;
+    unsigned long long wait_ns;  // limit of every wait (2 s outside the bounded-wait test)
+    int stall_after;             // the producers stop after this many loads (< 0: never)
 };
-
-__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
-    const unsigned long long t0 = globaltimer_ns();
-    while (!mbar_try_wait(bar, parity)) {
-        if (globaltimer_ns() - t0 > kDrainNs) return;
-    }
-}
 
 __device__ __forceinline__ float4 ld_shared_cluster_v4(uint32_t addr) {
     float4 v;
@@ -207,30 +200,24 @@ __global__ void __launch_bounds__(Cfg<BQ>::kThreads, BQ >= 128 ? 1 : 2)
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
 
+    int issued = 0;  // loads, by the producer's elected lane
     if (warp == kWarpTma) {
         // ---------------------------------------------------------------- producer --
-        long long issued = 0;
         bool ok = true;
         for (int i = 0; i < ng; ++i) {
             const int stage = i % ST;
-            if (!mbar_wait_bounded(empty(stage), static_cast<uint32_t>(((i / ST) & 1) ^ 1), abort_flag)) {
+            ok &= wait_on(empty(stage), static_cast<uint32_t>(((i / ST) & 1) ^ 1), abort_flag, a.wait_ns);
+            if (ok && i == a.stall_after) {  // the bounded-wait test: stop issuing
+                stall_until_abort(abort_flag, 4 * a.wait_ns);
                 ok = false;
-                break;
             }
-            if (elect_one()) {
+            if (elect_one() && ok) {
                 mbar_arrive_expect_tx(full(stage), C::kStageBytes);
                 tma_load_2d(sP + stage * C::kPBytes, &tmap_p, full(stage), (g0 + i) * kG, static_cast<int>(p0));
                 tma_load_2d(sQ + stage * C::kQBytes, &tmap_q, full(stage), (g0 + i) * kG, static_cast<int>(q0));
+                issued = i + 1;
             }
             __syncwarp();
-            ++issued;
-        }
-        if (!ok) {
-            // wait for every load still in flight before the block may go on
-            for (int s = 0; s < ST; ++s) {
-                const long long fills = (issued - s + ST - 1) / ST;
-                if (fills > 0) drain_wait(full(s), static_cast<uint32_t>((fills - 1) & 1));
-            }
         }
     } else if (warp == kWarpMma) {
         // -------------------------------------------------------------- MMA issuer --
@@ -238,13 +225,10 @@ __global__ void __launch_bounds__(Cfg<BQ>::kThreads, BQ >= 128 ? 1 : 2)
         bool ok = true;
         for (int i = 0; i < ng; ++i) {
             const int stage = i % ST, buf = i % NB;
-            if (!mbar_wait_bounded(full(stage), static_cast<uint32_t>((i / ST) & 1), abort_flag) ||
-                !mbar_wait_bounded(tempty(buf), static_cast<uint32_t>(((i / NB) & 1) ^ 1), abort_flag)) {
-                ok = false;
-                break;
-            }
+            ok &= wait_on(full(stage), static_cast<uint32_t>((i / ST) & 1), abort_flag, a.wait_ns);
+            ok &= wait_on(tempty(buf), static_cast<uint32_t>(((i / NB) & 1) ^ 1), abort_flag, a.wait_ns);
             tc_fence_after();
-            if (elect_one()) {
+            if (elect_one() && ok) {
                 const uint32_t pa = sP + stage * C::kPBytes, qa = sQ + stage * C::kQBytes;
 #pragma unroll
                 for (int kk = 0; kk < kG / 32; ++kk)
@@ -255,18 +239,13 @@ __global__ void __launch_bounds__(Cfg<BQ>::kThreads, BQ >= 128 ? 1 : 2)
             }
             __syncwarp();
         }
-        if (!ok) {
-            if (elect_one()) tc_commit(drain_bar);
-            __syncwarp();
-            drain_wait(drain_bar, 0);
-        }
     } else if (warp == kWarpScale) {
         // -------------------------------------------------------------- scales --
         // rows past an edge take the last row's scale; they are not stored
         for (int i = 0; i < ng; ++i) {
             const int slot = i % kScaleSlots;
-            if (!mbar_wait_bounded(sempty(slot), static_cast<uint32_t>(((i / kScaleSlots) & 1) ^ 1), abort_flag))
-                break;
+            if (!wait_on(sempty(slot), static_cast<uint32_t>(((i / kScaleSlots) & 1) ^ 1), abort_flag, a.wait_ns))
+                break;  // a lane alone may: nothing here wants the warp whole
             const uint32_t dst = sScale + static_cast<uint32_t>(slot * C::kSlotFloats * 4);
             const int64_t g = g0 + i;
 #pragma unroll
@@ -295,11 +274,8 @@ __global__ void __launch_bounds__(Cfg<BQ>::kThreads, BQ >= 128 ? 1 : 2)
         bool ok = true;
         for (int i = 0; i < ng; ++i) {
             const int slot = i % kScaleSlots, buf = i % NB;
-            if (!mbar_wait_bounded(sfull(slot), static_cast<uint32_t>((i / kScaleSlots) & 1), abort_flag) ||
-                !mbar_wait_bounded(tfull(buf), static_cast<uint32_t>((i / NB) & 1), abort_flag)) {
-                ok = false;
-                break;
-            }
+            ok &= wait_on(sfull(slot), static_cast<uint32_t>((i / kScaleSlots) & 1), abort_flag, a.wait_ns);
+            ok &= wait_on(tfull(buf), static_cast<uint32_t>((i / NB) & 1), abort_flag, a.wait_ns);
             tc_fence_after();
             const float* sc = scales + slot * C::kSlotFloats;
             const uint64_t sp2 = pack_f32x2(sc[BQ + r], sc[BQ + r]);
@@ -331,7 +307,7 @@ __global__ void __launch_bounds__(Cfg<BQ>::kThreads, BQ >= 128 ? 1 : 2)
             __syncwarp();
             if (lane == 0) mbar_arrive(sempty(slot));
         }
-        if (ok) {
+        if (__all_sync(0xFFFFFFFFu, ok)) {
             float y[C::kCols];
 #pragma unroll
             for (int j = 0; j < C::kCols / 2; ++j) {
@@ -364,6 +340,20 @@ __global__ void __launch_bounds__(Cfg<BQ>::kThreads, BQ >= 128 ? 1 : 2)
 
     tc_fence_before();
     __syncthreads();
+    if (*abort_flag) {
+        // a role gave up: all have ended, with loads and MMAs possibly in flight
+        if (warp == kWarpTma && elect_one()) {
+            for (int s = 0; s < ST; ++s) {
+                const int fills = fills_of(issued, ST, s);
+                if (fills > 0) drain_wait(full(s), static_cast<uint32_t>((fills - 1) & 1));
+            }
+        } else if (warp == kWarpMma) {
+            if (elect_one()) tc_commit(drain_bar);
+            __syncwarp();
+            drain_wait(drain_bar, 0);
+        }
+        __syncthreads();
+    }
     if (nsplit > 1) {
         // every block's partial sums are in its shared memory: the blocks share out the columns,
         // and a thread adds four neighbouring rows of Pm over the blocks, in their order, with
@@ -423,15 +413,14 @@ cudaError_t launch_bq(const Fp8Product& d, int split, cudaStream_t stream) {
         return cudaFuncSetAttribute(fp8_gemm_kernel<BQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
     });
     if (e != cudaSuccess) return e;
-    const Args a{d, groups, per, static_cast<int>(tiles_q)};
+    const WaitTest wt = wait_test();
+    const Args a{d, groups, per, static_cast<int>(tiles_q), wt.wait_ns, wt.stall_after};
     return launch_pdl(fp8_gemm_kernel<BQ>, dim3(static_cast<unsigned>(tiles_p * tiles_q * split)), dim3(C::kThreads),
                       C::kSmemBytes, stream, split > 1 ? dim3(static_cast<unsigned>(split), 1, 1) : dim3(kNoCluster),
                       tq, tp, a, split);
 }
 
 }  // namespace
-
-cudaError_t launch_fp8_product_pair(const Fp8Product& d, int tile_p, int sms, cudaStream_t stream);
 
 // Which kernel runs a product: the one with the least expected time, in microseconds.  The rates
 // come from timing both sides of every choice on rows 1 .. 2048 of six weight shapes (512 x 256

@@ -17,7 +17,9 @@
 // 4-11 run the epilogue.  Loads and MMAs are issued by an elected lane of a warp whose lanes
 // all run the loop: issued from a branch of one lane, four MMAs and two commits took 590
 // cycles against 230, more than the tensor pipe needs for them.  The register file is split
-// by setmaxnreg.  All waits are bounded as in the ternary kernels; no load uses multicast.
+// by setmaxnreg.  All waits are bounded as in the ternary kernels; a pair that gives up (see
+// bl_fp8.cuh) lets its roles run out and waits for its loads and MMAs in flight.  No load uses
+// multicast.
 //
 // Measured (bf16 output): 8192 x 8640 x 3200 in 216 us, 2.10 PFLOP/s; with the epilogue taken
 // out, loads and MMAs alone run at 3.05.  What is left is the hand-over of the two
@@ -34,9 +36,6 @@
 #include "bl_internal.h"
 
 namespace bl {
-
-bool encode_tmap_u8_pitch(CUtensorMap* map, const void* ptr, uint64_t inner, uint64_t outer, uint64_t pitch,
-                          uint32_t box_inner, uint32_t box_outer);
 
 namespace {
 
@@ -58,19 +57,20 @@ struct Cfg {
     static constexpr int kSlotFloats = kHalf + TP;
     static constexpr int kBars = 2 * kStages + 2 * kBufs + 2 * kSlots + 1;
     static constexpr int kSmemBytes = 1024 + kStages * (kQBytes + kPBytes) + kEpiWarps * kTurnBytes +
-                                      kSlots * kSlotFloats * 4 + 8 * kBars + 16;
+                                      kSlots * kSlotFloats * 4 + 8 * kBars + 16;  // and three words
     static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 };
 // the first four warps give up registers for the epilogue's sums: 128 * 56 + 256 * 224 is the
 // 384 * 168 that the block is launched with
 constexpr int kRegsLaunch = 168, kRegsSmall = 56, kRegsEpi = 224;
 static_assert(128 * kRegsSmall + 256 * kRegsEpi <= kThreads * kRegsLaunch, "register split");
-constexpr unsigned long long kDrainNs = 200000000ull;
 
 struct Args {
     Fp8Product d;
     int groups;
     int tiles_q, tiles_p, num_tiles;
+    unsigned long long wait_ns;  // limit of every wait (2 s outside the bounded-wait test)
+    int stall_after;             // the producers stop after this many loads (< 0: never)
 };
 
 // Tiles in panels of kPanel tiles along q, p running inside a panel: the tiles in flight share
@@ -85,11 +85,17 @@ __device__ __forceinline__ void tile_origin(const Args& a, int tp, int tile, int
     p0 = static_cast<int64_t>(rest / high) * tp;
 }
 
-__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
-    const unsigned long long t0 = globaltimer_ns();
-    while (!mbar_try_wait(bar, parity)) {
-        if (globaltimer_ns() - t0 > kDrainNs) return;
-    }
+// Shared variables of another CTA of the cluster, and a barrier's bytes of a load that never came.
+__device__ __forceinline__ void st_shared_cluster(uint32_t addr, int v) {
+    asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ int ld_shared_cluster(uint32_t addr) {
+    int v;
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ void mbar_complete_tx(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cluster.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -192,6 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t drain_bar = sBar + 8u * (C::kBars - 1);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + (sBar - base) + 8 * C::kBars);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    volatile int* issued_loads = reinterpret_cast<volatile int*>(tmem_slot + 2);  // by this CTA's producer
     const float* scales = reinterpret_cast<const float*>(gbase + (sScale - base));
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -235,39 +242,35 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ------------------------------------------------------------ producer --
             int stage = 0;
             uint32_t phase = 0;
-            long long issued = 0;
+            int issued = 0;
             bool ok = true;
-            for (int tile = first; ok && tile < a.num_tiles; tile += step) {
+            for (int tile = first; tile < a.num_tiles; tile += step) {
                 int64_t q0, p0;
                 tile_origin(a, TP, tile, q0, p0);
                 const int qr = static_cast<int>(q0) + kHalf * static_cast<int>(rank);
                 const int pr = static_cast<int>(p0) + TP / 2 * static_cast<int>(rank);
                 for (int g = 0; g < a.groups; ++g) {
-                    if (!mbar_wait_cluster_bounded(empty(stage), phase ^ 1u, abort_flag)) {
+                    ok &= wait_on(empty(stage), phase ^ 1u, abort_flag, a.wait_ns);
+                    if (ok && issued == a.stall_after) {  // the bounded-wait test: stop issuing
+                        stall_until_abort(abort_flag, 4 * a.wait_ns);
                         ok = false;
-                        break;
                     }
-                    if (elect_one()) {
+                    issued += ok;
+                    if (elect_one() && ok) {
                         if (leader) mbar_arrive_expect_tx(full(stage), 2 * (C::kQBytes + C::kPBytes));
                         const uint32_t bar = mapa_shared(full(stage), 0);
                         tma_load_2d_pair(sQ + stage * C::kQBytes, &tmap_q, bar, g * kG, qr);
                         tma_load_2d_pair(sP + stage * C::kPBytes, &tmap_p, bar, g * kG, pr);
                     }
                     __syncwarp();
-                    ++issued;
                     if (++stage == ST) {
                         stage = 0;
                         phase ^= 1u;
                     }
                 }
             }
-            if (!ok && leader) {
-                // both CTAs' loads are counted on this CTA's barriers
-                for (int s = 0; s < ST; ++s) {
-                    const long long fills = (issued - s + ST - 1) / ST;
-                    if (fills > 0) drain_wait(full(s), static_cast<uint32_t>((fills - 1) & 1));
-                }
-            }
+            if (elect_one()) *issued_loads = issued;
+            __syncwarp();
         } else if (warp == kWarpScale) {
             // -------------------------------------------------------------- scales --
             // rows past an edge take the last row's scale; they are not stored
@@ -279,8 +282,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tile_origin(a, TP, tile, q0, p0);
                 q0 += kHalf * static_cast<int>(rank);
                 for (int g = 0; g < a.groups; ++g) {
-                    if (!mbar_wait_bounded(sempty(slot), phase ^ 1u, abort_flag)) {
-                        ok = false;
+                    if (!wait_on(sempty(slot), phase ^ 1u, abort_flag, a.wait_ns)) {
+                        ok = false;  // a lane alone may leave: nothing here wants the warp whole
                         break;
                     }
                     const uint32_t dst = sScale + static_cast<uint32_t>(slot * C::kSlotFloats * 4 + 4 * lane);
@@ -313,15 +316,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             int stage = 0, buf = 0;
             uint32_t phase = 0, bphase = 0;
             bool ok = true;
-            for (int tile = first; ok && tile < a.num_tiles; tile += step) {
+            for (int tile = first; tile < a.num_tiles; tile += step) {
                 for (int g = 0; g < a.groups; ++g) {
-                    if (!mbar_wait_cluster_bounded(full(stage), phase, abort_flag) ||
-                        !mbar_wait_cluster_bounded(tempty(buf), bphase ^ 1u, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
+                    ok &= wait_on(full(stage), phase, abort_flag, a.wait_ns);
+                    ok &= wait_on(tempty(buf), bphase ^ 1u, abort_flag, a.wait_ns);
                     tc_fence_after();
-                    if (elect_one()) {
+                    if (elect_one() && ok) {
                         const uint32_t qa = sQ + stage * C::kQBytes, pa = sP + stage * C::kPBytes;
 #pragma unroll
                         for (int kk = 0; kk < kG / 32; ++kk)
@@ -343,11 +343,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            if (!ok) {
-                if (elect_one()) tc_commit_pair_multicast(drain_bar, 0x1);
-                __syncwarp();
-                drain_wait(drain_bar, 0);
-            }
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEpi));
@@ -367,16 +362,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int j = 0; j < kCols; ++j) acc[j] = 0.0f;
             for (int g = 0; g < a.groups; ++g) {
-                if (!mbar_wait_bounded(sfull(slot), sphase, abort_flag)) {
-                    ok = false;
-                    break;
-                }
+                ok &= wait_on(sfull(slot), sphase, abort_flag, a.wait_ns);
                 const float* sc = scales + slot * C::kSlotFloats;
                 const float fq = sc[r] * (ROWS ? 1.0f : sc[kHalf + block * kCols / 128]);
-                if (!mbar_wait_cluster_bounded(tfull(buf), bphase, abort_flag)) {
-                    ok = false;
-                    break;
-                }
+                ok &= wait_on(tfull(buf), bphase, abort_flag, a.wait_ns);
                 tc_fence_after();
                 const uint32_t addr = t_addr + static_cast<uint32_t>(buf * TP);
                 // the next 32 columns are on their way while these are scaled
@@ -420,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     bphase ^= 1u;
                 }
             }
-            if (!ok) break;
+            if (!__all_sync(0xFFFFFFFFu, ok)) break;
             int64_t q0, p0;
             tile_origin(a, TP, tile, q0, p0);
             q0 += kHalf * static_cast<int>(rank) + 32 * quarter;
@@ -434,7 +423,32 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     tc_fence_before();
     __syncthreads();
+    if (threadIdx.x == 0 && *abort_flag) st_shared_cluster(mapa_shared(smem_u32(const_cast<int*>(abort_flag)), rank ^ 1u), 1);
     cluster_sync_all();  // no CTA leaves while its peer may still signal its barriers
+    if (*abort_flag) {
+        // A role of either CTA gave up, and every role of both has ended, with loads and MMAs possibly
+        // in flight.  Both CTAs' loads are counted on the even one's barriers, which expect both: a
+        // stage that only one of them has filled (neither is ahead by more than one round of a stage,
+        // which takes the MMAs of the round before) is made up for.
+        if (leader && warp == kWarpTma) {
+            const int mine = *issued_loads;
+            const int peer = ld_shared_cluster(mapa_shared(smem_u32(const_cast<int*>(issued_loads)), 1));
+            for (int s = 0; s < ST; ++s) {
+                const int fills = fills_of(mine, ST, s), other = fills_of(peer, ST, s);
+                if (lane == 0 && fills > other) mbar_complete_tx(full(s), C::kQBytes + C::kPBytes);
+                if (lane == 0 && fills < other) mbar_arrive_expect_tx(full(s), C::kQBytes + C::kPBytes);
+                __syncwarp();
+                const int rounds = fills > other ? fills : other;
+                if (rounds > 0) drain_wait(full(s), static_cast<uint32_t>((rounds - 1) & 1));
+            }
+        } else if (leader && warp == kWarpMma) {
+            if (elect_one()) tc_commit_pair_multicast(drain_bar, 0x1);
+            __syncwarp();
+            drain_wait(drain_bar, 0);
+        }
+        __syncthreads();
+        cluster_sync_all();
+    }
     if (warp == kWarpMma) {
         tc_fence_after();
         tmem_dealloc_pair(tmem_base, 512);
@@ -455,12 +469,18 @@ cudaError_t launch(const Fp8Product& d, int sms, cudaStream_t stream) {
         return cudaErrorInvalidValue;
     static PerContextOnce attr;
     cudaError_t e = attr.run([] {
+        // the split of the registers takes all that the block is launched with
+        cudaFuncAttributes f;
+        const cudaError_t e = cudaFuncGetAttributes(&f, fp8_gemm2_kernel<ROWS, TP>);
+        if (e != cudaSuccess) return e;
+        if (f.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;
         return cudaFuncSetAttribute(fp8_gemm2_kernel<ROWS, TP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     C::kSmemBytes);
     });
     if (e != cudaSuccess) return e;
+    const WaitTest wt = wait_test();
     const Args a{d, static_cast<int>((d.C + kG - 1) / kG), static_cast<int>(tiles_q), static_cast<int>(tiles_p),
-                 static_cast<int>(tiles_q * tiles_p)};
+                 static_cast<int>(tiles_q * tiles_p), wt.wait_ns, wt.stall_after};
     const int pairs = a.num_tiles < sms / 2 ? a.num_tiles : sms / 2;
     return launch_pdl(fp8_gemm2_kernel<ROWS, TP>, dim3(static_cast<unsigned>(2 * pairs)), dim3(kThreads),
                       C::kSmemBytes, stream, dim3(2, 1, 1), tq, tp, a);
