@@ -431,6 +431,22 @@ BL_API bl_status bitlinear_norm_backward(const void *dY, bl_dtype dy_dtype, cons
                                          float norm_eps, void *dX, bl_dtype dx_dtype, float *dweight, float *dbias,
                                          void *ws, size_t ws_bytes, int32_t *err_word, void *stream);
 
+/* A test of the backward's bounded device waits: bitlinear_norm_backward in which every wait
+ * gives up after wait_limit_ns (0 < wait_limit_ns <= 2 s; the backward uses 2 s) and the warp
+ * that loads the rows of a block stops after stall_after_loads loads of one or several rows.
+ * The waits for the next load then run out: the kernel comes to its end with every copy in
+ * flight waited for, ORs BL_ERRBIT_TIMEOUT into err_word and returns; the outputs are left
+ * incomplete.  If no block needs more loads than stall_after_loads, or the rows are too long
+ * to be loaded so (K > 77696), it finishes normally.  The next call on the stream runs as
+ * usual.  Errors: those of bitlinear_norm_backward; BL_ERR_INVALID_ARG for a limit out of
+ * range. */
+BL_API bl_status bitlinear_norm_backward_stall_test(const void *dY, bl_dtype dy_dtype, const void *X,
+                                                    bl_dtype x_dtype, const float *norm_weight, int64_t M, int64_t K,
+                                                    bl_norm_kind norm_kind, float norm_eps, void *dX,
+                                                    bl_dtype dx_dtype, float *dweight, float *dbias, void *ws,
+                                                    size_t ws_bytes, int32_t *err_word, uint64_t wait_limit_ns,
+                                                    int32_t stall_after_loads, void *stream);
+
 /* ----------------------------------------------------------------------------------
  * 8-bit floating-point product with a scale for each block of 128, for the layers of a
  * b1.58 model that are left unternarised (an output head, or any matrix whose codes would

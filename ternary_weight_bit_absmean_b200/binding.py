@@ -39,7 +39,7 @@ EXPORTED = [
     "bitlinear_norm_forward", "bitlinear_norm_backward_workspace_size", "bitlinear_norm_backward",
     "bitlinear_fp8_row_bytes", "bitlinear_fp8_quantize_act", "bitlinear_fp8_quantize_weights",
     "bitlinear_fp8_forward", "bitlinear_fp8_backward_input", "bitlinear_fp8_backward_weight",
-    "bitlinear_fp8_stall_test",
+    "bitlinear_fp8_stall_test", "bitlinear_norm_backward_stall_test",
     "bitlinear_last_cuda_error",
     "bitlinear_status_string",
 ]
@@ -111,6 +111,9 @@ def lib() -> ctypes.CDLL:
         L.bitlinear_norm_backward_workspace_size.restype = ctypes.c_size_t
         L.bitlinear_norm_backward.argtypes = [P, S, P, S, P, I64, I64, S, F, P, S, P, P, P, ctypes.c_size_t, P, P]
         L.bitlinear_norm_backward.restype = S
+        L.bitlinear_norm_backward_stall_test.argtypes = [P, S, P, S, P, I64, I64, S, F, P, S, P, P, P, ctypes.c_size_t, P,
+                                                         ctypes.c_uint64, ctypes.c_int32, P]
+        L.bitlinear_norm_backward_stall_test.restype = S
         L.bitlinear_fp8_row_bytes.argtypes = [I64]
         L.bitlinear_fp8_row_bytes.restype = I64
         L.bitlinear_fp8_quantize_act.argtypes = [P, S, I64, I64, F, P, P, P, P, P]
@@ -428,6 +431,20 @@ def bitlinear_norm_backward(dY, X, norm_weight, kind, norm_eps, dX, dweight, dbi
         None if ws is None else _ptr(ws, torch.uint8, "ws"), 0 if ws is None else ws.numel(),
         _opt(err_word, "err_word"), _here(dY)),
         "bitlinear_norm_backward")
+
+
+@_scoped
+def bitlinear_norm_backward_stall_test(dY, X, norm_weight, kind, norm_eps, dX, dweight, dbias, ws, err_word,
+                                       wait_limit_ns, stall_after_loads):
+    """The norm's backward with every device wait limited to wait_limit_ns and the loads of each
+    block's rows stopped after stall_after_loads of them (a test of the bounded waits)."""
+    M, K = _matrix(X, "X")
+    _check(lib().bitlinear_norm_backward_stall_test(
+        *_float(dY, "dY", (M, K)), *_float(X, "X"), _vec(norm_weight, "norm_weight", K), M, K, int(kind),
+        float(norm_eps), *_float(dX, "dX", (M, K)), _vec(dweight, "dweight", K), _vec(dbias, "dbias", K),
+        None if ws is None else _ptr(ws, torch.uint8, "ws"), 0 if ws is None else ws.numel(),
+        _opt(err_word, "err_word"), int(wait_limit_ns), int(stall_after_loads), _here(dY)),
+        "bitlinear_norm_backward_stall_test")
 
 
 def bitlinear_fp8_row_bytes(K: int) -> int:

@@ -23,7 +23,7 @@ LIB = os.path.join(PKG, "libbitlinear.so")
 DEBUG_LIB = os.path.join(PKG, "libbitlinear_debug.so")
 SOURCES = ["bl_api.cu", "k_quant.cu", "k_gemv.cu", "k_gemv_tma.cu", "k_gemv_tc.cu", "k_gemv_stream.cu", "k_gemm_tc.cu", "k_gemm_tc2.cu", "bl_noalloc.cu", "k_tl5.cu", "k_ste.cu",
            "k_norm.cu", "k_fp8_quant.cu", "k_fp8_gemm.cu", "k_fp8_gemm2.cu"]
-HEADERS = ["bl_device.cuh", "bl_fp8.cuh", "bl_internal.h"]
+HEADERS = ["bl_device.cuh", "bl_fp8.cuh", "bl_wait.cuh", "bl_internal.h"]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",

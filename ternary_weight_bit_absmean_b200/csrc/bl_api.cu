@@ -405,6 +405,22 @@ bl_status bitlinear_norm_backward(const void* dY, bl_dtype dy_dtype, const void*
                                                 dweight, dbias, ws, err_word, as_stream(stream)));
 }
 
+bl_status bitlinear_norm_backward_stall_test(const void* dY, bl_dtype dy_dtype, const void* X, bl_dtype x_dtype,
+                                             const float* norm_weight, int64_t M, int64_t K, bl_norm_kind norm_kind,
+                                             float norm_eps, void* dX, bl_dtype dx_dtype, float* dweight, float* dbias,
+                                             void* ws, size_t ws_bytes, int32_t* err_word, uint64_t wait_limit_ns,
+                                             int32_t stall_after_loads, void* stream) {
+    BL_RANGE("bitlinear_norm_backward_stall_test");
+    if (wait_limit_ns == 0 || wait_limit_ns > bl::kDefaultWaitNs || stall_after_loads < 0) return BL_ERR_INVALID_ARG;
+    const bl::WaitTest saved = bl::g_wait_test;
+    bl::g_wait_test = bl::WaitTest{wait_limit_ns, stall_after_loads};
+    const bl_status st =
+        bitlinear_norm_backward(dY, dy_dtype, X, x_dtype, norm_weight, M, K, norm_kind, norm_eps, dX, dx_dtype,
+                                dweight, dbias, ws, ws_bytes, err_word, stream);
+    bl::g_wait_test = saved;
+    return st;
+}
+
 int64_t bitlinear_fp8_row_bytes(int64_t K) { return K <= 0 ? 0 : bl::fp8_row_bytes(K); }
 
 // 448 / eps and eps / 448 have to stay ordinary fp32 numbers.

@@ -8,6 +8,7 @@
 #include <cuda_runtime.h>
 
 #include "bl_device.cuh"
+#include "bl_wait.cuh"
 
 namespace bl {
 
@@ -106,38 +107,12 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
-// How the products' warps wait, and give a wait up.  The lanes of a warp poll a barrier and the abort
-// flag on their own, so some can see a phase complete while others give up, and what follows a wait
+// How the products' warps give a wait up.  The lanes of a warp poll a barrier and the abort flag on
+// their own (wait_on), so some can see a phase complete while others give up, and what follows a wait
 // (elect.sync, tcgen05.ld, __syncwarp) wants the warp whole.  So giving up ends no loop: the lane goes
-// along to the end with its `ok` false, looking at the flag before it waits for anything again; loads
-// and MMAs are issued where the elected lane's waits all succeeded, and results stored where every
-// lane's did.  (4096 x 4096 x 1536 34.1 us, its gradients 38 and 40; with a vote and a way out after
-// every wait instead 35.4, 40 and 43.)
-__device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int* abort,
-                                        unsigned long long limit_ns) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const unsigned long long t0 = globaltimer_ns();
-    const uint32_t hint = limit_ns < kSuspendHintNs ? static_cast<uint32_t>(limit_ns) : kSuspendHintNs;
-    do {
-        if (*abort) return false;
-        if (globaltimer_ns() - t0 > limit_ns) {
-            *abort = 1;
-            return false;
-        }
-    } while (!mbar_try_wait_sleep(bar, parity, hint));
-    return true;
-}
-
-// Wait for what is in flight after a wait was given up: the abort flag does not end this one.
-constexpr unsigned long long kDrainNs = 200000000ull;  // 0.2 s
-__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
-    const unsigned long long t0 = globaltimer_ns();
-    while (!mbar_try_wait(bar, parity)) {
-        if (globaltimer_ns() - t0 > kDrainNs) return;
-    }
-}
-// Of `issued` loads that went round `stages` stages in turn, the ones into stage s.
-__device__ __forceinline__ int fills_of(int issued, int stages, int s) { return (issued - s + stages - 1) / stages; }
+// along to the end with its `ok` false; loads and MMAs are issued where the elected lane's waits all
+// succeeded, and results stored where every lane's did.  (4096 x 4096 x 1536 34.1 us, its gradients 38
+// and 40; with a vote and a way out after every wait instead 35.4, 40 and 43.)
 
 // One product of the library in the kernels' terms:
 //   out[q, p] = sum_g sq[g, q] sp(g, p) sum_{c in group g} Qm[q, c] Pm[p, c]

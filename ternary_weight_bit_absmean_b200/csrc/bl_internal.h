@@ -158,10 +158,11 @@ cudaError_t launch_fp8_product(const Fp8Product& d, cudaStream_t stream);
 // Keep a CUDA error code for bitlinear_last_cuda_error() on the calling thread.
 void record_cuda_error(int code);
 
-// Limits of the device-side waits of the TMA-fed forward kernels and of the 8-bit products, as
-// the launchers copy them into the kernel arguments.  Outside a call of a stall test
-// (bitlinear_forward_stall_test, bitlinear_fp8_stall_test) they are {2 s, -1}: every wait gives
-// up after 2 s, and producers never stall.  Those test entry points set them on the calling thread for the duration of its call only: the
+// Limits of the device-side waits of the TMA-fed forward kernels, of the 8-bit products and of the
+// norm's backward, as the launchers copy them into the kernel arguments.  Outside a call of a
+// stall test (bitlinear_forward_stall_test, bitlinear_fp8_stall_test,
+// bitlinear_norm_backward_stall_test) they are {2 s, -1}: every wait gives up after 2 s, and
+// producers never stall.  Those test entry points set them on the calling thread for the duration of its call only: the
 // waits give up after wait_ns, and each block's producer stops issuing loads after
 // stall_after of them, so that the waits for the next load run out.
 struct WaitTest {

@@ -48,6 +48,7 @@
 
 #include "bl_device.cuh"
 #include "bl_internal.h"
+#include "bl_wait.cuh"
 
 namespace bl {
 namespace {
@@ -60,7 +61,7 @@ constexpr int kMaxThreads = 1024;
 constexpr int kMaxStages = 8;
 constexpr int kRingBytes = 208 * 1024;
 constexpr int kParts = 148;      // most blocks or clusters: one per SM
-constexpr unsigned long long kDrainNs = 200000000ull;
+constexpr unsigned long long kLandNs = 1000000ull;  // 1 ms: see Place::finish
 
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
@@ -525,6 +526,13 @@ struct Control {
     float4 cross_sums[2][kMaxCluster];
     float2 sums[kMaxGroups][64];
     int abort;
+    int issued;                           // loads of the ring
+    unsigned long long wait_ns;
+    // wait_on with the limit in shared memory, where it takes no registers (as an argument: 8192 x 4096
+    // layer bf16 82 us, so 72)
+    __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) {
+        return wait_on(bar, parity, &abort, [this] { return *static_cast<volatile unsigned long long*>(&wait_ns); });
+    }
 };
 
 // GroupSum, then over the blocks of the cluster (each sends its sums to all).  A slot is
@@ -565,11 +573,13 @@ struct RowSum {
         }
         return make_float3(all.x, all.y, first);
     }
+    // After a wait was given up nothing is sent or expected any more (the slot's phase before may not have
+    // ended), and the other blocks give up in turn.
     __device__ __forceinline__ void exchange(uint32_t call, const float4& own) {
         const int slot = static_cast<int>(call & 1), t = local.t;
         const uint32_t bar = smem_u32(&ctl->cross[slot]);
-        if (t == 0) mbar_arrive_expect_tx(bar, 16u * static_cast<uint32_t>(cluster));
-        if (t < cluster) {
+        if (t < cluster && !*static_cast<volatile int*>(&ctl->abort)) {
+            if (t == 0) mbar_arrive_expect_tx(bar, 16u * static_cast<uint32_t>(cluster));
             const uint32_t dst = mapa_shared(smem_u32(&ctl->cross_sums[slot][rank]), static_cast<uint32_t>(t));
             const uint32_t rbar = mapa_shared(bar, static_cast<uint32_t>(t));
             asm volatile(
@@ -578,16 +588,9 @@ struct RowSum {
                 "r"(__float_as_uint(own.w)), "r"(rbar)
                 : "memory");
         }
-        mbar_wait_bounded(bar, (call >> 1) & 1u, &ctl->abort);
+        ctl->wait(bar, (call >> 1) & 1u);
     }
 };
-
-__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
-    const unsigned long long t0 = globaltimer_ns();
-    while (!mbar_try_wait(bar, parity)) {
-        if (globaltimer_ns() - t0 > kDrainNs) return;
-    }
-}
 
 __device__ __forceinline__ uint32_t cluster_size() {
     uint32_t r;
@@ -605,7 +608,7 @@ struct Place {
     uint32_t rank;
     int64_t first, step;  // its batches start at rows first, first + step, ...
     int k0, ks;           // its columns
-    __device__ __forceinline__ Place(uint8_t* smem, const Shape& s) {
+    __device__ __forceinline__ Place(uint8_t* smem, const Shape& s, unsigned long long wait_ns) {
         ctl = reinterpret_cast<Control*>(smem);
         ring = smem + ((sizeof(Control) + 127) & ~size_t(127));
         tpr = s.tpr;
@@ -625,7 +628,8 @@ struct Place {
             }
             mbar_init(smem_u32(&ctl->cross[0]), 1);
             mbar_init(smem_u32(&ctl->cross[1]), 1);
-            ctl->abort = 0;
+            ctl->abort = ctl->issued = 0;
+            ctl->wait_ns = wait_ns;
             mbar_fence_init();
         }
         pdl_wait_then_release();
@@ -643,25 +647,39 @@ struct Place {
         if (end > most) end = most;
         if (end < begin) end = begin;
     }
-    __device__ __forceinline__ void finish(int32_t* err) const {
+    __device__ __forceinline__ void finish(const Shape& s, int32_t* err) const {
         __syncthreads();
-        if (cluster > 1) cluster_sync_all();  // nobody's sums are still on their way here
-        if (threadIdx.x == 0 && *static_cast<volatile int*>(&ctl->abort) && err != nullptr)
-            atomicOr(err, kErrBitTimeout);
+        if (cluster > 1) cluster_sync_all();
+        if (threadIdx.x == 0 && *static_cast<volatile int*>(&ctl->abort)) {
+            // a wait was given up: loads of the ring may be in flight
+            for (int i = 0; i < s.stages; ++i) {
+                const int fills = fills_of(ctl->issued, s.stages, i);
+                if (fills > 0) drain_wait(smem_u32(&ctl->full[i]), static_cast<uint32_t>((fills - 1) & 1));
+            }
+            // And sums of the cluster's other blocks, which have all ended.  How many they sent before
+            // they gave up is not known here, so the block stays until they must have landed.  (A block
+            // that has not given up has waited for every sum that was sent to it.)
+            const unsigned long long t0 = globaltimer_ns();
+            while (cluster > 1 && globaltimer_ns() - t0 < kLandNs) {
+            }
+            if (err != nullptr) atomicOr(err, kErrBitTimeout);
+        }
     }
 };
 
 // One lane fills the ring, in the order in which the batches are worked on.
 template <typename TX, typename TD>
-__device__ __forceinline__ void fill_ring(const Place& pl, const Shape& s, const TX* X, const TD* dY) {
+__device__ __forceinline__ void fill_ring(const Place& pl, const Shape& s, const TX* X, const TD* dY,
+                                          unsigned long long wait_ns, int stall_after) {
     if (threadIdx.x % 32 != 0) return;
-    long long issued = 0;
-    bool ok = true;
+    int issued = 0;
     for (int64_t m = pl.first; m < s.M; m += pl.step, ++issued) {
-        const int stage = static_cast<int>(issued % s.stages);
-        if (!mbar_wait_bounded(smem_u32(&pl.ctl->empty[stage]), static_cast<uint32_t>(((issued / s.stages) & 1) ^ 1),
-                               &pl.ctl->abort)) {
-            ok = false;
+        const int stage = issued % s.stages;
+        if (!wait_on(smem_u32(&pl.ctl->empty[stage]), static_cast<uint32_t>(((issued / s.stages) & 1) ^ 1),
+                     &pl.ctl->abort, wait_ns))
+            break;
+        if (issued == stall_after) {  // the bounded-wait test: stop issuing
+            stall_until_abort(&pl.ctl->abort, 4 * wait_ns);
             break;
         }
         const uint32_t bar = smem_u32(&pl.ctl->full[stage]);
@@ -684,11 +702,7 @@ __device__ __forceinline__ void fill_ring(const Place& pl, const Shape& s, const
             bulk_load(slot + s.slot_x, dY + begin, n * static_cast<uint32_t>(sizeof(TD)), bar);
         }
     }
-    if (!ok)  // wait for the copies in flight before the block may leave
-        for (int i = 0; i < s.stages; ++i) {
-            const long long fills = (issued - i + s.stages - 1) / s.stages;
-            if (fills > 0) drain_wait(smem_u32(&pl.ctl->full[i]), static_cast<uint32_t>((fills - 1) & 1));
-        }
+    pl.ctl->issued = issued;
 }
 
 struct BwdArgs {
@@ -700,6 +714,8 @@ struct BwdArgs {
     float* dw;  // [blocks or clusters, K] partial sums (the result itself with one), or NULL
     float* db;
     int32_t* err;
+    unsigned long long wait_ns;  // limit of every wait (2 s outside the bounded-wait test)
+    int stall_after;             // the ring's producers stop after this many loads (< 0: never)
 };
 
 // LAYER: the kind, known when compiling, so that RMS rows pay nothing for the mean (8192 x 8640: 121
@@ -710,7 +726,7 @@ __global__ void __launch_bounds__(THREADS)
     extern __shared__ __align__(128) uint8_t smem[];
     constexpr bool kHalves = THREADS < 640 || CH == 1;
     const Shape& s = a.s;
-    Place pl(smem, s);
+    Place pl(smem, s, a.wait_ns);
     const int t = pl.t, tpr = pl.tpr;
     // this thread's columns: element 0 of chunk c is column k0 + (c tpr + t) 8 - skip
     const int skip = EDGE ? static_cast<int>(((pl.first + pl.group) * s.K + pl.k0) & (kE - 1)) : 0;
@@ -729,7 +745,7 @@ __global__ void __launch_bounds__(THREADS)
             if constexpr (DB) db[c][e] = 0.0f;
         }
     if (pl.producer) {
-        fill_ring<TX, TD>(pl, s, X, dY);
+        fill_ring<TX, TD>(pl, s, X, dY, a.wait_ns, a.stall_after);
     } else {
         RowSum<kHalves> row_sum{GroupSum<kHalves>{pl.ctl->sums[pl.group], t, tpr, pl.group}, pl.ctl, pl.cluster,
                                 pl.rank};
@@ -758,7 +774,7 @@ __global__ void __launch_bounds__(THREADS)
         for (int64_t m = pl.first + pl.group; m - pl.group < s.M; m += pl.step, flat += flat_step) {
             // a wait that gives up does not end the loop (the group's barriers would no longer match):
             // the rest runs on what is there, and the block reports it at the end
-            mbar_wait_bounded(smem_u32(&pl.ctl->full[stage]), phase, &pl.ctl->abort);
+            pl.ctl->wait(smem_u32(&pl.ctl->full[stage]), phase);
             const bool live = m < s.M;
             const uint8_t* slot = pl.ring + stage * (s.slot_x + s.slot_d);
             Raw<TX> x[CH];
@@ -909,7 +925,7 @@ __global__ void __launch_bounds__(THREADS)
             if constexpr (DB) a.db[off + k] = sb;
         }
     }
-    pl.finish(a.err);
+    pl.finish(s, a.err);
 }
 
 struct LongBwdArgs {
@@ -1196,7 +1212,8 @@ cudaError_t backward_t(const TX* X, const TD* dY, const BwdCall& c, cudaStream_t
                           dim3(kNoCluster), X, dY, a, static_cast<const float4*>(c.stats), rows);
     }
     const Plan p = plan_of(c.M, c.K, sizeof(TX), sizeof(TD));
-    const BwdArgs a{p.s, c.w, c.eps, inv_k, c.dx, c.dx_bf16, c.dw, c.db, c.err};
+    const WaitTest wt = wait_test();
+    const BwdArgs a{p.s, c.w, c.eps, inv_k, c.dx, c.dx_bf16, c.dw, c.db, c.err, wt.wait_ns, wt.stall_after};
     if (c.K % kE == 0)
         return c.layer ? backward_e<TX, TD, false, true>(X, dY, p, a, stream)
                        : backward_e<TX, TD, false, false>(X, dY, p, a, stream);

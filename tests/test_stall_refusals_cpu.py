@@ -25,3 +25,12 @@ def test_fp8_stall_test_refusals(L):
     for i, v, want in [(10, 0, INVALID), (10, 2_000_000_001, INVALID), (11, -1, INVALID), (0, None, INVALID),
                        (4, 0, INVALID), (8, 2, INVALID), (7, FAKE + 4, MISALIGNED)]:
         assert f(*replaced(good, i, v)) == want, (i, v)
+
+
+def test_norm_backward_stall_test_refusals(L):
+    f = L.bitlinear_norm_backward_stall_test
+    #       dY    type X     type w     M  K    kind eps   dX    type dw    db    ws    bytes    err   limit      stall stream
+    good = [FAKE, 0, FAKE, 0, FAKE, 8, 64, 1, 1e-5, FAKE, 0, FAKE, FAKE, FAKE, 1 << 20, None, 1_000_000, 1, None]
+    for i, v, want in [(16, 0, INVALID), (16, 2_000_000_001, INVALID), (17, -1, INVALID), (0, None, INVALID),
+                       (5, 0, INVALID), (7, 2, INVALID), (9, FAKE + 4, MISALIGNED)]:
+        assert f(*replaced(good, i, v)) == want, (i, v)
