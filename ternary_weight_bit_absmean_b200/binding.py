@@ -474,20 +474,26 @@ def bitlinear_fp8_quantize_weights(W, eps, wq_out, s_out, wqt_out=None):
         _here(W)), "bitlinear_fp8_quantize_weights")
 
 
-def _codes_of(left, right, names):
-    """Rows of two code matrices and the bytes of their rows.  The padding behind a row is
-    zero, so the padded length serves as the contraction's."""
+def _codes_of(left, right, names, length=None):
+    """Rows of two code matrices and the length of the contraction: `length`, or the padded length
+    of their rows, which gives the same where the codes behind `length` are zeros, as the
+    quantisers leave them."""
     rows_l, n = _matrix(left, names[0])
     rows_r, n_r = _matrix(right, names[1])
     if n != n_r or n % 16 != 0:
         raise ValueError("%s and %s must have rows of the same multiple of 16 codes, got %d and %d"
                          % (*names, n, n_r))
-    return rows_l, rows_r, n
+    if length is None:
+        return rows_l, rows_r, n
+    length = int(length)
+    if length < 1 or _up16(length) != n:
+        raise ValueError("rows of %d codes do not hold %d and their padding to a multiple of 16" % (n, length))
+    return rows_l, rows_r, length
 
 
 @_scoped
-def bitlinear_fp8_forward(xq, sx, wq, sw, out, err_word=None):
-    M, N, K = _codes_of(xq, wq, ("xq", "wq"))
+def bitlinear_fp8_forward(xq, sx, wq, sw, out, err_word=None, K=None):
+    M, N, K = _codes_of(xq, wq, ("xq", "wq"), K)
     _check(lib().bitlinear_fp8_forward(
         _ptr(xq, _E4M3, "xq"), _ptr(sx, torch.float32, "sx", (_blocks(K), M)), _ptr(wq, _E4M3, "wq"),
         _ptr(sw, torch.float32, "sw", (_blocks(N), _blocks(K))), M, N, K, *_float(out, "out", (M, N)),
@@ -507,8 +513,8 @@ def bitlinear_fp8_stall_test(xq, sx, wq, sw, out, err_word, wait_limit_ns, stall
 
 
 @_scoped
-def bitlinear_fp8_backward_input(dyq, sdy, wqt, sw, dX, err_word=None):
-    M, K, N = _codes_of(dyq, wqt, ("dyq", "wqt"))
+def bitlinear_fp8_backward_input(dyq, sdy, wqt, sw, dX, err_word=None, N=None):
+    M, K, N = _codes_of(dyq, wqt, ("dyq", "wqt"), N)
     _check(lib().bitlinear_fp8_backward_input(
         _ptr(dyq, _E4M3, "dyq"), _ptr(sdy, torch.float32, "sdy", (_blocks(N), M)), _ptr(wqt, _E4M3, "wqt"),
         _ptr(sw, torch.float32, "sw", (_blocks(N), _blocks(K))), M, N, K, *_float(dX, "dX", (M, K)),
@@ -516,8 +522,8 @@ def bitlinear_fp8_backward_input(dyq, sdy, wqt, sw, dX, err_word=None):
 
 
 @_scoped
-def bitlinear_fp8_backward_weight(dyqt, sdyt, xqt, sxt, dW, err_word=None):
-    N, K, M = _codes_of(dyqt, xqt, ("dyqt", "xqt"))
+def bitlinear_fp8_backward_weight(dyqt, sdyt, xqt, sxt, dW, err_word=None, M=None):
+    N, K, M = _codes_of(dyqt, xqt, ("dyqt", "xqt"), M)
     _check(lib().bitlinear_fp8_backward_weight(
         _ptr(dyqt, _E4M3, "dyqt"), _ptr(sdyt, torch.float32, "sdyt", (_blocks(M), N)), _ptr(xqt, _E4M3, "xqt"),
         _ptr(sxt, torch.float32, "sxt", (_blocks(M), K)), M, N, K, *_float(dW, "dW", (N, K)),
@@ -652,24 +658,28 @@ def fp8_quantize_weights(W: torch.Tensor, eps: float = 1e-5, transposed: bool = 
 
 
 @_scoped
-def fp8_forward(xq, sx, wq, sw, out_dtype=torch.float32, err_word=None):
-    """y [M, N] = x w^T from the codes and scales of fp8_quantize_act and fp8_quantize_weights."""
+def fp8_forward(xq, sx, wq, sw, out_dtype=torch.float32, err_word=None, K=None):
+    """y [M, N] = x w^T from the codes and scales of fp8_quantize_act and fp8_quantize_weights.
+    Without K, whole rows of codes are contracted: what pads them to a multiple of 16 must be
+    zeros (the quantisers' is).  With K it is not read."""
     out = sx.new_empty((xq.shape[0], wq.shape[0]), dtype=out_dtype)
-    bitlinear_fp8_forward.__wrapped__(xq, sx, wq, sw, out, err_word)
+    bitlinear_fp8_forward.__wrapped__(xq, sx, wq, sw, out, err_word, K)
     return out
 
 
 @_scoped
-def fp8_backward_input(dyq, sdy, wqt, sw, out_dtype=torch.float32, err_word=None):
-    """dX [M, K] = dY w from the gradient's codes and the transposed weight codes."""
+def fp8_backward_input(dyq, sdy, wqt, sw, out_dtype=torch.float32, err_word=None, N=None):
+    """dX [M, K] = dY w from the gradient's codes and the transposed weight codes.  Without N, what
+    pads their rows must be zeros (see fp8_forward)."""
     dX = sdy.new_empty((dyq.shape[0], wqt.shape[0]), dtype=out_dtype)
-    bitlinear_fp8_backward_input.__wrapped__(dyq, sdy, wqt, sw, dX, err_word)
+    bitlinear_fp8_backward_input.__wrapped__(dyq, sdy, wqt, sw, dX, err_word, N)
     return dX
 
 
 @_scoped
-def fp8_backward_weight(dyqt, sdyt, xqt, sxt, out_dtype=torch.float32, err_word=None):
-    """dW [N, K] = dY^T x from the transposed codes of the gradient and the activations."""
+def fp8_backward_weight(dyqt, sdyt, xqt, sxt, out_dtype=torch.float32, err_word=None, M=None):
+    """dW [N, K] = dY^T x from the transposed codes of the gradient and the activations.  Without M,
+    what pads their rows must be zeros (see fp8_forward)."""
     dW = sdyt.new_empty((dyqt.shape[0], xqt.shape[0]), dtype=out_dtype)
-    bitlinear_fp8_backward_weight.__wrapped__(dyqt, sdyt, xqt, sxt, dW, err_word)
+    bitlinear_fp8_backward_weight.__wrapped__(dyqt, sdyt, xqt, sxt, dW, err_word, M)
     return dW
