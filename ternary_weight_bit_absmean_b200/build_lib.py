@@ -14,6 +14,7 @@ runtime's driver entry point), so it loads on a machine without a GPU.
 import os
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -60,23 +61,43 @@ def up_to_date(lib: str = LIB) -> bool:
     return all(os.path.getmtime(p) <= t for p in _inputs())
 
 
+def free_memory() -> int:
+    """Bytes that a new process can have without swapping (0 if the system does not say)."""
+    try:
+        with open("/proc/meminfo") as f:
+            return next((int(line.split()[1]) * 1024 for line in f if line.startswith("MemAvailable:")), 0)
+    except OSError:
+        return 0
+
+
+def jobs() -> int:
+    """Compilers to run at a time: one per core that this process may use and per GB of free memory
+    (the largest file takes 0.62 GB), BL_BUILD_JOBS at most if that is set."""
+    n = min(len(SOURCES), len(os.sched_getaffinity(0)), free_memory() >> 30)
+    return max(1, min(n, int(os.environ.get("BL_BUILD_JOBS") or n)))
+
+
 def build(force: bool = False, verbose: bool = False, debug: bool = False) -> str:
     lib = DEBUG_LIB if debug else LIB
     if not force and up_to_date(lib):
         return lib
     objdir = os.path.join(PKG, "_build_debug" if debug else "_build")
     os.makedirs(objdir, exist_ok=True)
-    objs, running = [], []
-    for src in SOURCES:  # one compiler per file, side by side
+    objs, cmds = [], []
+    for src in SOURCES:
         obj = os.path.join(objdir, src.replace(".cu", ".o"))
         cmd = [NVCC, *FLAGS, *(["-DBL_DEBUG_CHECKS=1"] if debug else []), "-I", INCLUDE, "-I", CSRC, "-c",
                os.path.join(CSRC, src), "-o", obj]
         if verbose:
             cmd.insert(1, "-Xptxas=-v")
-        running.append((cmd, subprocess.Popen(cmd)))
+        cmds.append(cmd)
         objs.append(obj)
-    # wait for all of them before complaining about one
-    for cmd, code in [(cmd, proc.wait()) for cmd, proc in running]:
+    # one compiler per file, the largest files first; all of them have ended before one that failed
+    # is complained about
+    cmds.sort(key=lambda cmd: -os.path.getsize(cmd[-3]))
+    with ThreadPoolExecutor(max_workers=jobs()) as pool:
+        codes = list(pool.map(lambda cmd: subprocess.run(cmd).returncode, cmds))
+    for cmd, code in zip(cmds, codes):
         if code != 0:
             raise subprocess.CalledProcessError(code, cmd)
     tmp = lib + ".tmp.%d" % os.getpid()
