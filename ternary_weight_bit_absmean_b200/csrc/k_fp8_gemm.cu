@@ -276,6 +276,7 @@ __global__ void __launch_bounds__(Cfg<BQ>::kThreads, BQ >= 128 ? 1 : 2)
             const int slot = i % kScaleSlots, buf = i % NB;
             ok &= wait_on(sfull(slot), static_cast<uint32_t>((i / kScaleSlots) & 1), abort_flag, a.wait_ns);
             ok &= wait_on(tfull(buf), static_cast<uint32_t>((i / NB) & 1), abort_flag, a.wait_ns);
+            __syncwarp();  // the lanes' polls may have ended at different times
             tc_fence_after();
             const float* sc = scales + slot * C::kSlotFloats;
             const uint64_t sp2 = pack_f32x2(sc[BQ + r], sc[BQ + r]);

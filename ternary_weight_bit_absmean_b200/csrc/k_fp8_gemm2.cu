@@ -366,6 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float* sc = scales + slot * C::kSlotFloats;
                 const float fq = sc[r] * (ROWS ? 1.0f : sc[kHalf + block * kCols / 128]);
                 ok &= wait_on(tfull(buf), bphase, abort_flag, a.wait_ns);
+                __syncwarp();  // the lanes' polls may have ended at different times
                 tc_fence_after();
                 const uint32_t addr = t_addr + static_cast<uint32_t>(buf * TP);
                 // the next 32 columns are on their way while these are scaled
