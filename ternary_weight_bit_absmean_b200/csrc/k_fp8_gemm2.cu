@@ -21,8 +21,9 @@
 // bl_fp8.cuh) lets its roles run out and waits for its loads and MMAs in flight.  No load uses
 // multicast.
 //
-// Measured (bf16 output): 8192 x 8640 x 3200 in 216 us, 2.10 PFLOP/s; with the epilogue taken
-// out, loads and MMAs alone run at 3.05.  What is left is the hand-over of the two
+// Measured (bf16 output): 8192 x 8640 x 3200 in 222 us on a cool GPU, 2.04 PFLOP/s, and up to 245
+// where the power limit has lowered the clock (260 a call in a loop of calls); with the epilogue
+// taken out, loads and MMAs alone run at 3.05 PFLOP/s.  What is left is the hand-over of the two
 // accumulators (an accumulator is busy for its MMAs, the commit, the readers' 430 cycles and
 // their signal back: about 1660 cycles for two groups on an idle GPU) and the clock, which
 // the power limit lowers.

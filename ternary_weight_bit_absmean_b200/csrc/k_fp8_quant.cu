@@ -1,8 +1,7 @@
 // k_fp8_quant.cu -- e4m3 codes with one fp32 scale for each block of 128, the operands of
-// the 8-bit floating-point product (k_fp8_gemm.cu) for layers that are left unternarised
-// ("1.58 bits: what BitNet promised and what it required": not every matrix of a b1.58
-// model is ternary; "1-bit & Ternary LLMs", block "BitNet (Oct 2023)": absmax scaling to
-// the largest code, no zero point).
+// the 8-bit floating-point product (k_fp8_gemm.cu) for layers that are left unternarised.
+// Scaling by the largest magnitude to the largest code, without a zero point, as the int8
+// quantiser does ("1-bit & Ternary LLMs", block "BitNet (Oct 2023)").
 //
 //   a = max |x| over the block (a NaN stays one),  m = max(a, eps)
 //   d = m / 448,   code = e4m3(x * (448 / m))      (IEEE fp32 quotients and product, then

@@ -22,8 +22,8 @@
 //   mean_k (x - mean)^2 = mean_k c^2 - lo^2,   mean_k(g n) = (mean_k(g c) - lo mean_k g) r
 // where lo is what rounding the mean to fp32 leaves over.  The differences are right to half a unit
 // of their own, so what is left is the rounding of a sum of them, whatever the mean; a constant
-// row's are all zero.  Cost: one subtraction an element (8192 x 8192 bf16 with a bias: forward 52.0
-// -> 54.5 us, backward 113.5 -> 116.2).
+// row's are all zero.  Cost: one subtraction an element (8192 x 8192 bf16 with a bias: forward 52
+// -> 55 us, backward 113.5 -> 116.5).
 //
 // Both are bound by memory: a row is read once, held in registers as it came, and written once.
 // A matrix is cut into chunks of eight elements of its flat order, whatever K is, so that every
@@ -251,9 +251,10 @@ __device__ __forceinline__ void load_vector(const float* p, float fill, int64_t 
 
 // Sums of two values over the threads of a group.  Slots alternate between calls: one is written
 // again only after a barrier that every reader of it has passed.  HALVES: each half of a warp adds
-// one of the two, which takes half the exchanges and some registers (backward of 8192 x 3200 layer
-// bf16 84 -> 77 us; in the widest blocks, whose registers are short, 142 -> 164 for 8192 x 8640 RMS
-// fp32, so these add both in every lane).
+// one of the two, which takes half the exchanges and some registers (backward of 8192 x 8192 layer
+// fp32 193 -> 142 us, 4096 x 16384 241 -> 177; the 640 threads with two chunks, whose registers are
+// short, add both in every lane: 8192 x 4096 layer bf16 72 us, with halves 75, 8192 x 8640 RMS 120
+// and 123).
 template <bool HALVES>
 struct GroupSum {
     float2* buf;  // [2][32] of this group
@@ -757,7 +758,7 @@ __global__ void __launch_bounds__(THREADS)
         const int at = static_cast<int>((pl.first + pl.group) * s.K + pl.k0 - skip - (row0 & ~int64_t(kE - 1))) + t * kE;
         int64_t flat = (pl.first + pl.group) * s.K + pl.k0 - skip + t * kE;  // of chunk 0, in the matrix
         const int64_t flat_step = pl.step * s.K;
-        // values converted once with one chunk; with two that costs more (123 -> 133 us for 8192 x
+        // values converted once with one chunk; with two that costs more (120 -> 131 us for 8192 x
         // 8640 RMS), and the raw chunk is converted in each pass
         constexpr bool kOnce = CH == 1;
         // Two chunks, both gradients and both sums in 96 registers: held from one pass to the next, the
@@ -1084,12 +1085,12 @@ cudaError_t forward_x(const TX* X, const FwdArgs& a, cudaStream_t stream) {
 // A thread owns one chunk in rows of up to 384 and two or three above.  What decides is how many warps
 // the registers of its columns (x, dy, w, dw and with a bias db) leave room for: a warp too many on
 // one of the SM's four schedulers takes registers from all of them, and the sums spill.
-//   - two chunks from there to 4096 columns, so that two rows fit a block: 8192 x 3200 RMS 60 -> 47 us,
-//     layer fp32 85 -> 62 (4096 layer fp32 loses, 102 -> 114).  With fewer rows than SMs one chunk is
-//     quicker (32 x 4096: 6.6 against 6.1 us).
+//   - two chunks from there to 4096 columns, so that two rows fit a block: 8192 x 3200 RMS 54 -> 48 us,
+//     layer fp32 93 -> 65, 8192 x 4096 layer bf16 86 -> 72 (in fp32 it loses, 105 -> 118).  With fewer
+//     rows than SMs one chunk is quicker (32 x 4096: 6.6 against 6.0 us).
 //   - three chunks where two would need sixteen warps beside the one that fills the ring: 8192 x 8192
-//     layer 232 -> 143 us in fp32, 131 -> 113 in bf16 (RMS loses, 121 -> 125; both must take the same
-//     so that leaving out db changes no bit of dw).
+//     layer 236 -> 142 us in fp32, 143 -> 117 in bf16 (RMS 116 either way).
+// The layout does not depend on which outputs are asked for, so leaving out db changes no bit of dw.
 struct Plan {
     int cluster, chunks;  // blocks of a row, chunks of a thread
     Shape s;
@@ -1163,9 +1164,10 @@ cudaError_t backward_c(const TX* X, const TD* dY, const Plan& p, const BwdArgs& 
 }
 
 // The kernel whose limit of threads leaves the most registers: 80 with up to 768, 128 with up to 512,
-// 168 with up to 384 (8192 x 7680 layer fp32 at 128 registers 134 us, at the 96 of 640 threads 210).
-// Without a bias 96 do, and what more there is only lets the compiler move loads (8192 x 7680 RMS:
-// 104 against 116 us).
+// 168 with up to 384 (8192 x 7680 layer fp32 at 128 registers 142 us, at the 96 of 640 threads 219).
+// Without a bias 96 are enough for rows of whole chunks (up to 80 bytes spill in fp32, up to 160 in
+// other rows), and what more there is only lets the compiler move loads (8192 x 7680 RMS: 101 against
+// 110 us).
 template <typename TX, typename TD, bool EDGE, bool LAYER>
 cudaError_t backward_e(const TX* X, const TD* dY, const Plan& p, const BwdArgs& a, cudaStream_t stream) {
     if (a.db != nullptr) {
