@@ -1086,8 +1086,9 @@ cudaError_t forward_x(const TX* X, const FwdArgs& a, cudaStream_t stream) {
 // the registers of its columns (x, dy, w, dw and with a bias db) leave room for: a warp too many on
 // one of the SM's four schedulers takes registers from all of them, and the sums spill.
 //   - two chunks from there to 4096 columns, so that two rows fit a block: 8192 x 3200 RMS 54 -> 48 us,
-//     layer fp32 93 -> 65, 8192 x 4096 layer bf16 86 -> 72 (in fp32 it loses, 105 -> 118).  With fewer
-//     rows than SMs one chunk is quicker (32 x 4096: 6.6 against 6.0 us).
+//     layer fp32 93 -> 65, 8192 x 4096 layer bf16 86 -> 72 (in fp32 with a bias it loses, 105 -> 118,
+//     without one it gains, 118 -> 108).  With fewer rows than SMs one chunk is quicker (32 x 4096: 6.6
+//     against 6.0 us).
 //   - three chunks where two would need sixteen warps beside the one that fills the ring: 8192 x 8192
 //     layer 236 -> 142 us in fp32, 143 -> 117 in bf16 (RMS 116 either way).
 // The layout does not depend on which outputs are asked for, so leaving out db changes no bit of dw.
